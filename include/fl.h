@@ -501,6 +501,116 @@ typedef struct {
 /* Several K-quant tensors in one launch (a decode step); no workspace. */
 FL_API fl_status fl_gemv_kquant_batched(const fl_kquant_problem* problems, int n, int batch, void* stream);
 
+/* ========================================================================= */
+/* Paged key/value cache ([FoQLens] progress table, "a format of our own": one */
+/* stored copy, any depth read from it; here for the cached tokens instead of  */
+/* the weights). A page holds 64 tokens' keys and values for every key/value  */
+/* head, as 8-bit codes split into a high and a low nibble plane, so a block   */
+/* of 64 tokens is read at its own depth: level 0 ZERO (not read, not          */
+/* visible), 1-2 D4 (top four bits), 3 and above D8.                          */
+/*   stored   a = max_d |x_d| over the head's D values, scale = a / 127 (one   */
+/*            IEEE fp32 division), code_d = rint(127 x_d / a) (0 when a = 0),  */
+/*            u = code + 128 = 16 h + l; bit for bit reproducible. A row that  */
+/*            holds an infinity or a NaN is stored as scale NaN, codes 0.      */
+/*   value    D8: scale code;  D4: scale (16 (h - 8) + 7.5) (the low nibble's  */
+/*            centre, as the plane products read it)                           */
+/*                                                                           */
+/* Layout (this library's own): page p, key/value head c at byte               */
+/* (p kv_heads + c) R, R = 512 + 128 D:                                        */
+/*   [0, 256)  fp32 key scale of slot j at 4 j;  [256, 512)  value scales      */
+/*   512 + 32 D i, 32 D bytes each: i = 0 keys' high nibbles, 1 values' high,  */
+/*   2 keys' low, 3 values' low (a D4 read is the contiguous prefix of         */
+/*   512 + 64 D bytes). Element (slot j, dim d) of a plane:                    */
+/*     keys:   byte 16 (32 (D/64 ((j/4) % 4) + d/64) + 4 g + (d % 64) / 16)    */
+/*             + 8 ((j/2) % 2) + 4 ((d % 16) / 8) + n / 2,  nibble n % 2,      */
+/*             g = 2 (j/16) + j % 2,  n = (d % 8) / 2 + 4 (d % 2)              */
+/*     values: byte 16 (32 (d/16) + 4 (d % 8) + j/16) + 4 ((j/4) % 4)          */
+/*             + (j % 4) / 2 + 2 (j % 2),  nibble (d/8) % 2                    */
+/*   (nibble 0 = bits 0-3). Both are the order in which the attention's        */
+/*   tensor-core fragments take them.                                          */
+/* ========================================================================= */
+#define FL_KV_BLOCK 64          /* tokens per page */
+#define FL_KV_MAX_SEQS 1024     /* sequences per call */
+#define FL_ATTN_MAX_GROUP 32    /* query heads per key/value head */
+
+/* Bytes of one page (head_dim 64 or 128, 1 <= kv_heads <= 256); 0 for an invalid shape. */
+FL_API size_t fl_kv_page_bytes(int kv_heads, int head_dim);
+
+/* pages: device, num_pages * fl_kv_page_bytes(kv_heads, head_dim) bytes, 16-byte aligned. Any
+ * content is valid; slots behind a sequence's last token are never used. */
+typedef struct {
+  uint8_t* pages;
+  int num_pages;
+  int kv_heads;
+  int head_dim;
+} fl_kv_cache;
+
+/* The sequences of one call. Sequence i holds lens[i] tokens in the cache, its new ones included;
+ * its n_i = new_start[i + 1] - new_start[i] new tokens are its LAST n_i tokens and use rows
+ * new_start[i] .. new_start[i + 1] - 1 of the call's row buffers. new_start NULL: one new token per
+ * sequence, sequence i at row i (none where lens[i] is 0). Token at position t of sequence i lies in
+ * slot t % 64 of page block_table[i][t / 64].
+ *   block_table  device int32 [n_seqs][max_blocks]
+ *   lens         device int32 [n_seqs], 0 .. 64 max_blocks
+ *   new_start    device int32 [n_seqs + 1], non-decreasing, within 0 .. rows; or NULL
+ *   n_seqs       1 .. FL_KV_MAX_SEQS;  max_blocks 1 .. 2^23
+ *   rows         rows of the row buffers; rows outside every sequence's range are not touched
+ *   max_new      upper bound of every n_i (it sizes the launches and the workspace); max_new <= rows,
+ *                at most 2^22
+ * lens, new_start and the table are device data (a captured call may be replayed after they
+ * change), so the kernels check them: a sequence with n_i outside 0 .. min(max_new, lens[i]), rows
+ * or lens[i] out of range is left out of the call, a block whose page index is outside
+ * 0 .. num_pages - 1 is not read or written (it counts as ZERO), and the next fl_device_status()
+ * returns FL_ERR_ARG. Entries of the table that no listed token needs are not looked at. */
+typedef struct {
+  const int32_t* block_table;
+  const int32_t* lens;
+  const int32_t* new_start;
+  int n_seqs;
+  int max_blocks;
+  int rows;
+  int max_new;
+} fl_kv_batch;
+
+/* Quantise the new tokens' keys and values into their slots (formula above); every other slot keeps
+ * its bytes. k, v: device bf16 [rows][kv_heads][head_dim], row r at k + r * k_stride (in elements;
+ * strides are multiples of 8, at least kv_heads * head_dim, so both may lie in one fused
+ * projection's output), 16-byte aligned. Two new tokens of one call must not share a slot. One
+ * launch. */
+FL_API fl_status fl_kv_append(const fl_kv_cache* cache, const fl_kv_batch* batch, const uint16_t* k, int64_t k_stride,
+                              const uint16_t* v, int64_t v_stride, void* stream);
+
+/* Read the sequences' last n_i tokens back as bf16 (the value above, rounded to nearest even; ZERO
+ * blocks as 0). levels: device uint8 [n_seqs][max_blocks] or NULL (every block D8). k, v, strides as
+ * fl_kv_append, written. One launch. */
+FL_API fl_status fl_kv_read(const fl_kv_cache* cache, const fl_kv_batch* batch, const uint8_t* levels, uint16_t* k,
+                            int64_t k_stride, uint16_t* v, int64_t v_stride, void* stream);
+
+/* Attention of every sequence's new tokens over its cached tokens (appended before this call).
+ * Query head h reads key/value head h / (heads / kv_heads). The query at position p sees key j when
+ *   j <= p,  level of block j/64 > 0,  and  window == 0, or p - j < window, or j < sinks
+ *   out = sum_j e^(z_j - m) v_j / sum_j e^(z_j - m),  z_j = scale q . k_j,  m = max z;  0 when the
+ *   query sees no key (a ZERO level on its blocks).
+ * A key that a query does not see has no influence on its output, whatever its values (NaN among
+ * them). Arithmetic: products of bf16 queries with exact codes, accumulated in fp32; the softmax
+ * statistics in fp32; each probability times its value scale is rounded to bf16 before the second
+ * product, the output to bf16. Equal inputs give equal bits.
+ *   levels     device uint8 [n_seqs][max_blocks] or NULL (every block D8)
+ *   q, out     device bf16 [rows][heads][head_dim], row strides in elements (multiples of 8, at least
+ *              heads * head_dim), 16-byte aligned; out may be q
+ *   heads      a multiple of kv_heads, at most FL_ATTN_MAX_GROUP * kv_heads
+ *   scale      finite;  window >= 0;  sinks >= 0 (read only with a window)
+ *   workspace  at least fl_attn_workspace_bytes(n_seqs, heads, kv_heads, head_dim, max_new) bytes,
+ *              16-byte aligned, ZERO-FILLED before its first use; every completed call leaves its
+ *              counters at zero. Calls that share a workspace must not overlap on the GPU.
+ * fl_attn_workspace_bytes is 0 for an invalid shape (and without a device). */
+FL_API size_t fl_attn_workspace_bytes(int n_seqs, int heads, int kv_heads, int head_dim, int max_new);
+
+FL_API fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* batch, const uint8_t* levels,
+                               const uint16_t* q, int64_t q_stride, int heads, float scale, int window, int sinks,
+                               uint16_t* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
 #ifdef __cplusplus
 }
 #endif

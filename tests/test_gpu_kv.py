@@ -1,0 +1,557 @@
+"""The paged key/value cache and its attention on the GPU against the 64-bit reference, through the C-ABI.
+
+Cache bytes and read-back values are compared bit for bit. An attention output may be off by the
+bound that oracle.kv.attention derives: half a bf16 step on the output and on every probability
+times its value's scale (2^-8 relative each), and fp32 sums of the scores' and the outputs'
+lengths."""
+import numpy as np
+import pytest
+
+from oracle import kv
+from variable_precision_weight_b200 import synth
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from variable_precision_weight_b200 import build
+    build.build()
+    from variable_precision_weight_b200 import fl
+    torch.cuda.set_device(0)
+    return torch, fl
+
+
+def dev(torch, a):
+    a = np.ascontiguousarray(a)
+    return torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).cuda()
+
+
+def f64(bits):
+    return synth.bf16_bits_to_f32(np.asarray(bits).view(np.uint16)).astype(np.float64)
+
+
+class Case:
+    """A cache with random content (every slot of every page holds a quantised token), and a batch."""
+
+    def __init__(self, torch, fl, lens, news, kvh, D, seed, spare=2, width=None, rows=None, max_new=None,
+                 levels=None, spread=1.0):
+        g = np.random.default_rng(seed)
+        self.torch, self.fl, self.g, self.kvh, self.D = torch, fl, g, kvh, D
+        self.lens, self.news = list(lens), list(news)
+        blocks = [-(-n // 64) for n in lens]
+        self.num_pages = sum(blocks) + spare
+        self.width = width or max(blocks + [1])
+        order = g.permutation(self.num_pages)
+        self.table = np.full((len(lens), self.width), -7, np.int32)       # entries nobody needs are rubbish
+        at = 0
+        for i, b in enumerate(blocks):
+            self.table[i, :b] = order[at:at + b]
+            at += b
+        self.start = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        self.rows = rows or int(self.start[-1]) or 1
+        self.max_new = max_new or max(max(news), 1)
+        self.levels = None if levels is None else g.choice(levels, size=self.table.shape).astype(np.uint8)
+        rec = kv.record_bytes(D)
+        self.pages = g.integers(0, 256, (self.num_pages, kvh, rec), dtype=np.uint8)
+        sc = np.abs(g.standard_normal((self.num_pages, kvh, 128))).astype(np.float32) * np.float32(spread / 80) + \
+            np.float32(0.004)
+        self.pages[:, :, :512] = sc.view(np.uint8).reshape(self.num_pages, kvh, 512)
+        self.upload()
+
+    def upload(self):
+        t = self.torch
+        self.d_pages, self.d_table = dev(t, self.pages), dev(t, self.table)
+        self.d_lens, self.d_start = dev(t, np.array(self.lens, np.int32)), dev(t, self.start)
+        self.d_levels = None if self.levels is None else dev(t, self.levels)
+        self.cache = self.fl.kv_cache(self.d_pages, self.num_pages, self.kvh, self.D)
+        self.batch = self.fl.kv_batch(self.d_table, self.d_lens, self.d_start, len(self.lens), self.width, self.rows,
+                                      self.max_new)
+
+    def workspace(self, heads):
+        n = self.fl.fl_attn_workspace_bytes(len(self.lens), heads, self.kvh, self.D, self.max_new)
+        assert n > 0
+        return self.torch.zeros(n, dtype=self.torch.uint8, device="cuda"), n
+
+    def q(self, heads, gain=1.0):
+        return synth.f32_to_bf16_bits((gain * self.g.standard_normal((self.rows, heads, self.D))).astype(np.float32))
+
+    def attend(self, q, heads, scale, window=0, sinks=0, ws=None, out=None, stream=None):
+        t = self.torch
+        d_q = dev(t, q)
+        d_out = t.full((self.rows, heads, self.D), 77, dtype=t.int16, device="cuda") if out is None else out
+        ws, n = ws or self.workspace(heads)
+        w = heads * self.D
+        self.fl.fl_attn_paged(self.cache, self.batch, self.d_levels, d_q, w, heads, scale, window, sinks, d_out, w, ws,
+                              n, stream)
+        t.cuda.synchronize()
+        assert not ws[:2048].any()                                        # the counters are zero again
+        return d_out.cpu().numpy().view(np.uint16)
+
+    def check(self, got, q, heads, scale, window=0, sinks=0, skip=()):
+        gr = heads // self.kvh
+        worst = 0.0
+        for i, (n, new) in enumerate(zip(self.lens, self.news)):
+            if i in skip or new == 0:
+                continue
+            rows = slice(int(self.start[i]), int(self.start[i + 1]))
+            pos = np.arange(n - new, n)
+            for h in range(self.kvh):
+                k, v, lv, sc = kv.gather(self.pages, self.table[i], None if self.levels is None else self.levels[i], n,
+                                         self.D, h)
+                for x in range(h * gr, (h + 1) * gr):
+                    ref, tol = kv.attention(f64(q[rows, x]), k, v, lv, sc, pos, np.float32(scale), window, sinks)
+                    err = np.abs(f64(got[rows, x]) - ref)
+                    assert np.all(err <= tol), (i, x, float((err / tol).max()))
+                    worst = max(worst, float((err / tol).max()))
+        return worst
+
+    def untouched(self, got, fill=77):
+        """Rows outside every sequence keep what they held."""
+        live = np.zeros(self.rows, bool)
+        live[:self.start[-1]] = True
+        assert np.all(got[~live] == fill)
+
+
+# ------------------------------------------------------------------ append and read
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,news,kvh", [
+    ([1], [1], 1), ([64], [64], 2), ([65], [1], 3), ([64], [1], 1), ([130], [130], 1), ([70], [9], 2),
+    ([200, 0, 63, 129, 1], [137, 0, 2, 129, 1], 2), ([300, 300], [299, 1], 1)])
+def test_append_bit_exact(env, D, lens, news, kvh):
+    torch, fl = env
+    c = Case(torch, fl, lens, news, kvh, D, seed=D + sum(lens), rows=sum(news) + 2)
+    k, v = (synth.bf16_normal((c.rows, kvh, D), D, sum(lens), x) for x in (1, 2))
+    k[0, 0, :] = 0                                                        # an all-zero head
+    k[-3:, :, :4] = synth.f32_to_bf16_bits(np.array([127, -63.5, 0.5, 1.5], np.float32))   # ties
+    fl.fl_kv_append(c.cache, c.batch, dev(torch, k), kvh * D, dev(torch, v), kvh * D)
+    fl.fl_device_status()
+    want = c.pages.copy()
+    for i, (n, new) in enumerate(zip(lens, news)):
+        for x in range(new):
+            p, r = n - new + x, c.start[i] + x
+            for h in range(kvh):
+                (kc, ks), (vc, vs) = kv.quantise(f64(k[r, h])), kv.quantise(f64(v[r, h]))
+                kv.write_token(want[c.table[i, p // 64], h], D, p % 64, kc, ks, vc, vs)
+    assert np.array_equal(c.d_pages.cpu().numpy(), want)
+
+
+def test_append_strided_rows_and_non_finite(env):
+    """k and v inside one fused projection's rows; a row with an infinity or NaN is stored as scale NaN."""
+    torch, fl = env
+    kvh, D = 2, 64
+    c = Case(torch, fl, [40], [30], kvh, D, seed=3)
+    x = synth.bf16_normal((30, 4 * kvh * D + 8), 3, 1)
+    x[5, kvh * D + 3] = 0x7F80                                            # k row 5, head 0: infinity
+    x[6, 3 * kvh * D + D + 1] = 0xFFC1                                    # v row 6, head 1: NaN
+    d = dev(torch, x)
+    w = kvh * D
+    fl.fl_kv_append(c.cache, c.batch, d[:, w:], x.shape[1], d[:, 3 * w:], x.shape[1])
+    fl.fl_device_status()
+    got = c.d_pages.cpu().numpy()
+    for r in range(30):
+        for h in range(kvh):
+            rec = got[c.table[0, 0], h]
+            sc = rec[:512].view(np.float32).reshape(2, 64)[:, 10 + r]
+            ks, vs = (kv.quantise(f64(x[r, m * w + h * D:m * w + (h + 1) * D]))[1] for m in (1, 3))
+            assert np.array_equal(sc, [ks, vs], equal_nan=True), (r, h)
+            assert np.isnan(sc[0]) == (r == 5 and h == 0) and np.isnan(sc[1]) == (r == 6 and h == 1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,news,levels", [
+    ([1], [1], None), ([64, 65, 128], [64, 65, 1], None), ([500], [499], (0, 1, 2, 3, 4, 9)),
+    ([77, 0, 300], [3, 0, 211], (2, 4)), ([129], [100], (2,))])
+def test_read_bit_exact(env, D, lens, news, levels):
+    torch, fl = env
+    kvh = 2
+    c = Case(torch, fl, lens, news, kvh, D, seed=7 + D, levels=levels, rows=sum(news) + 1)
+    ko, vo = (torch.full((c.rows, kvh * D + 16), 55, dtype=torch.int16, device="cuda") for _ in "kv")
+    fl.fl_kv_read(c.cache, c.batch, c.d_levels, ko, kvh * D + 16, vo, kvh * D + 16)
+    fl.fl_device_status()
+    ko, vo = ko.cpu().numpy().view(np.uint16), vo.cpu().numpy().view(np.uint16)
+    assert np.all(ko[:, kvh * D:] == 55) and np.all(vo[:, kvh * D:] == 55)
+    assert np.all(ko[c.start[-1]:] == 55)
+    for i, (n, new) in enumerate(zip(lens, news)):
+        for h in range(kvh):
+            k, v, _, _ = kv.gather(c.pages, c.table[i], None if levels is None else c.levels[i], n, D, h)
+            for got, ref in ((ko, k), (vo, v)):
+                want = synth.f32_to_bf16_bits(ref[n - new:].astype(np.float32))
+                have = got[c.start[i]:c.start[i + 1], h * D:(h + 1) * D]
+                assert np.array_equal(have, want), (i, h)
+
+
+# ------------------------------------------------------------------ attention
+
+SHAPES = [  # kv heads, group, D
+    (1, 1, 64), (2, 2, 128), (2, 4, 64), (1, 3, 128), (1, 7, 64), (1, 8, 128), (1, 32, 64)]
+
+
+@pytest.mark.parametrize("kvh,group,D", SHAPES)
+@pytest.mark.parametrize("lens,news", [
+    ([1], [1]), ([64], [1]), ([65], [2]), ([1000], [1]), ([3, 700, 64, 129], [1, 1, 1, 1]), ([40, 0, 333], [8, 0, 5]),
+    ([517], [16])])
+def test_attend_short_chunks(env, kvh, group, D, lens, news):
+    torch, fl = env
+    heads = kvh * group
+    c = Case(torch, fl, lens, news, kvh, D, seed=group + sum(lens), rows=sum(news) + 3)
+    q = c.q(heads)
+    got = c.attend(q, heads, D ** -0.5)
+    fl.fl_device_status()
+    c.check(got, q, heads, D ** -0.5)
+    c.untouched(got)
+
+
+@pytest.mark.parametrize("kvh,group,D", [(2, 2, 128), (2, 4, 64), (1, 3, 64), (1, 1, 128)])
+@pytest.mark.parametrize("lens,news", [([150], [150]), ([300], [129]), ([64], [64]), ([257, 1, 90, 40], [200, 1, 33, 40]),
+                                       ([1100], [70]), ([513], [65])])
+@pytest.mark.parametrize("levels", [None, (2, 4)])
+def test_attend_prompt_chunks(env, kvh, group, D, lens, news, levels):
+    torch, fl = env
+    heads = kvh * group
+    c = Case(torch, fl, lens, news, kvh, D, seed=group + sum(news), rows=sum(news) + 5, levels=levels)
+    q = c.q(heads)
+    got = c.attend(q, heads, D ** -0.5)
+    fl.fl_device_status()
+    c.check(got, q, heads, D ** -0.5)
+    c.untouched(got)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (63, 0), (64, 4), (65, 64), (200, 65), (100, 5000), (5000, 4),
+                                          (2 ** 31 - 1, 2 ** 31 - 1)])
+@pytest.mark.parametrize("new", [1, 7, 150])
+def test_attend_window_and_sinks(env, window, sinks, new):
+    torch, fl = env
+    kvh, heads, D = 2, 4, 64
+    c = Case(torch, fl, [900, 151, 333], [new, new, 1], kvh, D, seed=window % 1000 + new, levels=(2, 4, 4))
+    q = c.q(heads)
+    got = c.attend(q, heads, 0.2, window, sinks)
+    fl.fl_device_status()
+    c.check(got, q, heads, 0.2, window, sinks)
+
+
+@pytest.mark.parametrize("levels", [(0,), (0, 2, 4), (0, 0, 0, 4), (1, 3), (2,), (0, 255)])
+@pytest.mark.parametrize("new", [1, 10, 140])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_levels_and_empty_rows(env, levels, new, D):
+    """Blocks at every level; queries whose every block is ZERO give exact zeros."""
+    torch, fl = env
+    kvh, heads = 2, 4
+    c = Case(torch, fl, [700, 140, 64 * 3], [new, new, new], kvh, D, seed=len(levels) + new, levels=levels)
+    q = c.q(heads)
+    got = c.attend(q, heads, D ** -0.5, 30 if new == 10 else 0, 0)
+    fl.fl_device_status()
+    c.check(got, q, heads, D ** -0.5, 30 if new == 10 else 0, 0)
+    if levels == (0,):
+        assert not got.any()
+
+
+@pytest.mark.parametrize("new", [1, 5, 130])
+def test_unseen_keys_have_no_influence(env, new):
+    """Slots behind the last token, keys after a query, and ZERO blocks hold NaN and infinite scales."""
+    torch, fl = env
+    kvh, heads, D = 2, 4, 128
+    c = Case(torch, fl, [330], [new], kvh, D, seed=11, levels=(4,))
+    c.levels[0, 1] = 0
+    c.upload()
+    q = c.q(heads)
+    clean = c.attend(q, heads, 0.09)
+    c.check(clean, q, heads, 0.09)
+    sc = c.pages[:, :, :512].view(np.float32).reshape(c.num_pages, kvh, 2, 64)
+    poison = np.where(np.arange(64) % 2, np.nan, np.inf).astype(np.float32)
+    sc[c.table[0, 1]] = poison                                    # the ZERO block
+    sc[c.table[0, 330 // 64], :, :, 330 % 64:] = poison[330 % 64:]  # behind the last token
+    unused = sorted(set(range(c.num_pages)) - set(c.table[0].tolist()))
+    sc[unused] = np.nan
+    c.upload()
+    assert np.array_equal(c.attend(q, heads, 0.09), clean)
+    # the newest token poisoned: only its own query sees it
+    sc[c.table[0, 329 // 64], :, :, 329 % 64] = np.nan
+    c.upload()
+    got = c.attend(q, heads, 0.09)
+    assert np.array_equal(got[:new - 1], clean[:new - 1]) and np.isnan(f64(got[new - 1])).all()
+
+
+def test_nan_query_stays_in_its_row(env):
+    torch, fl = env
+    for new in (9, 140):
+        c = Case(torch, fl, [200], [new], 2, 64, seed=new)
+        q = c.q(4)
+        clean = c.attend(q, 4, 0.1)
+        q2 = q.copy()
+        q2[3, 2, 5] = 0x7FC0
+        got = c.attend(q2, 4, 0.1)
+        hit = np.zeros(got.shape[:2], bool)
+        hit[3, 2] = True
+        assert np.isnan(f64(got[hit])).all() and np.array_equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("scale,gain", [(0.0, 1.0), (-0.3, 1.0), (30.0, 3.0), (1e-30, 1.0)])
+@pytest.mark.parametrize("new", [3, 140])
+def test_scales(env, scale, gain, new):
+    """Flat, negative and very sharp softmax (one key takes all)."""
+    torch, fl = env
+    c = Case(torch, fl, [500], [new], 1, 64, seed=5, levels=(2, 4))
+    q = c.q(2, gain)
+    c.check(c.attend(q, 2, scale), q, 2, scale)
+
+
+def test_new_start_omitted(env):
+    """One new token per sequence without new_start; an empty sequence's row keeps what it held."""
+    torch, fl = env
+    lens = [5, 0, 300, 64]
+    c = Case(torch, fl, lens, [1, 0, 1, 1], 2, 64, seed=2, rows=6, max_new=1)
+    c.batch = fl.kv_batch(c.d_table, c.d_lens, None, 4, c.width, c.rows, 1)
+    q = c.q(4)
+    got = c.attend(q, 4, 0.1)
+    fl.fl_device_status()
+    full = q.copy()
+    for i in (0, 2, 3):
+        for h in range(2):
+            k, v, lv, sc = kv.gather(c.pages, c.table[i], None, lens[i], 64, h)
+            for x in (2 * h, 2 * h + 1):
+                ref, tol = kv.attention(f64(full[i:i + 1, x]), k, v, lv, sc, np.array([lens[i] - 1]), np.float32(0.1), 0, 0)
+                assert np.all(np.abs(f64(got[i, x]) - ref[0]) <= tol[0])
+    assert np.all(got[[1, 4, 5]] == 77)
+    k = synth.bf16_normal((6, 2, 64), 2, 9)
+    fl.fl_kv_append(c.cache, c.batch, dev(torch, k), 128, dev(torch, k), 128)
+    ko, vo = (torch.full((6, 2, 64), 55, dtype=torch.int16, device="cuda") for _ in "kv")
+    fl.fl_kv_read(c.cache, c.batch, None, ko, 128, vo, 128)
+    fl.fl_device_status()
+    ko = ko.cpu().numpy().view(np.uint16)
+    assert np.all(ko[[1, 4, 5]] == 55) and torch.equal(vo.cpu(), torch.from_numpy(ko.view(np.int16)))
+    code, sc = kv.quantise(f64(k))
+    want = synth.f32_to_bf16_bits(sc[..., None] * code.astype(np.float32))
+    assert np.array_equal(ko[[0, 2, 3]], want[[0, 2, 3]])
+
+
+def test_strides_and_output_over_query(env):
+    """Queries inside wider rows; the output may be the query buffer."""
+    torch, fl = env
+    for new in (4, 150):
+        heads, D = 4, 64
+        c = Case(torch, fl, [260], [new], 2, D, seed=new)
+        wide = synth.bf16_normal((new, heads * D + 24), 9, new)
+        q = wide[:, 8:8 + heads * D].reshape(new, heads, D)
+        d = dev(torch, wide)
+        ws, n = c.workspace(heads)
+        stride = heads * D + 24
+        fl.fl_attn_paged(c.cache, c.batch, None, d[:, 8:], stride, heads, 0.1, 0, 0, d[:, 8:], stride, ws, n)
+        fl.fl_device_status()
+        out = d.cpu().numpy().view(np.uint16)
+        assert np.array_equal(out[:, :8], wide[:, :8]) and np.array_equal(out[:, 8 + heads * D:], wide[:, 8 + heads * D:])
+        c.check(out[:, 8:8 + heads * D].reshape(new, heads, D), q, heads, 0.1)
+
+
+def test_shared_prefix_pages(env):
+    """Two sequences whose first blocks are the same pages."""
+    torch, fl = env
+    c = Case(torch, fl, [400, 380], [3, 3], 2, 64, seed=8)
+    c.table[1, :4] = c.table[0, :4]
+    c.upload()
+    q = c.q(4)
+    c.check(c.attend(q, 4, 0.125), q, 4, 0.125)
+
+
+def test_equal_bits_and_reused_workspace(env):
+    """Calls of different shapes in a row on one workspace; the same call gives the same bits."""
+    torch, fl = env
+    cs = [Case(torch, fl, [3000, 70], [2, 2], 2, 128, seed=1), Case(torch, fl, [4100], [1], 2, 128, seed=2),
+          Case(torch, fl, [700], [300], 2, 128, seed=3)]
+    qs = [c.q(4) for c in cs]
+    n = max(c.workspace(4)[1] for c in cs)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    first = [c.attend(q, 4, 0.1, ws=(ws, n)) for c, q in zip(cs, qs)]
+    for c, q, f in zip(cs, qs, first):
+        c.check(f, q, 4, 0.1)
+    for _ in range(3):
+        for c, q, f in zip(cs, qs, first):
+            assert np.array_equal(c.attend(q, 4, 0.1, ws=(ws, n)), f)
+
+
+def test_bad_device_data_is_reported(env):
+    """Page indices, lengths and row ranges that the host cannot see: the block or sequence is left out."""
+    torch, fl = env
+    c = Case(torch, fl, [200, 100, 130], [2, 2, 2], 2, 64, seed=4)
+    q = c.q(4)
+    c.table[0, 1] = c.num_pages                                   # one past the last page
+    c.upload()
+    got = c.attend(q, 4, 0.1)
+    with pytest.raises(fl.FlError) as e:
+        fl.fl_device_status()
+    assert e.value.status == -1 and "page" in str(e.value)
+    fl.fl_device_status()
+    c.check(got, q, 4, 0.1)                                       # the reference reads that block as ZERO
+    for call in ("append", "read"):
+        x = torch.zeros((6, 2, 64), dtype=torch.int16, device="cuda")
+        before = c.d_pages.clone()
+        c.d_lens.copy_(torch.tensor([128, 100, 130], dtype=torch.int32))   # its new tokens lie in that block
+        if call == "append":
+            fl.fl_kv_append(c.cache, c.batch, x, 128, x, 128)
+        else:
+            fl.fl_kv_read(c.cache, c.batch, None, x, 128, x.clone(), 128)
+        with pytest.raises(fl.FlError):
+            fl.fl_device_status()
+        if call == "read":
+            assert torch.equal(before, c.d_pages)
+    c = Case(torch, fl, [200, 100, 130], [2, 2, 2], 2, 64, seed=4)
+    for lens, start in (([-1, 100, 130], [0, 2, 4, 6]), ([64 * c.width + 1, 100, 130], [0, 2, 4, 6]),
+                        ([1, 100, 130], [0, 2, 4, 6]), ([2 ** 31 - 1, 100, 130], [0, 2, 4, 6]),
+                        ([200, 100, 130], [0, 0, 4, 6]), ([200, 100, 130], [-2, 2, 4, 6]),
+                        ([200, 100, 130], [0, 2, 4, 7]), ([200, 100, 130], [5, 2, 4, 6])):
+        c.d_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        c.d_start.copy_(torch.tensor(start, dtype=torch.int32))
+        bad = [i for i in range(3) if not (0 <= lens[i] <= 64 * c.width and 0 <= start[i] <= start[i + 1] <= 6 and
+                                           start[i + 1] - start[i] <= min(2, lens[i]))]
+        got = c.attend(q, 4, 0.1)
+        with pytest.raises(fl.FlError) as e:
+            fl.fl_device_status()
+        assert e.value.status == -1 and "sequence" in str(e.value), (lens, start)
+        keep = (c.start, c.lens)
+        ok = [i for i in range(3) if i not in bad]
+        assert ok
+        for i in ok:
+            c.lens, c.start = lens, np.array(start, np.int32)
+            c.check(got, q, 4, 0.1, skip=[x for x in range(3) if x != i or start[i + 1] - start[i] != 2])
+        c.start, c.lens = keep
+
+
+def test_captured_calls_follow_device_lengths(env):
+    """Append, read and attention captured once; replayed after lens, rows and table change."""
+    torch, fl = env
+    kvh, heads, D = 2, 4, 64
+    c = Case(torch, fl, [300, 200, 100], [2, 60, 1], kvh, D, seed=6, rows=80, max_new=64, width=6)
+    k, v = (dev(torch, synth.bf16_normal((80, kvh, D), 6, x)) for x in (1, 2))
+    q = c.q(heads)
+    d_q, d_out = dev(torch, q), torch.full((80, heads, D), 77, dtype=torch.int16, device="cuda")
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    ws, n = c.workspace(heads)
+    w = heads * D
+
+    def calls(s=None):
+        fl.fl_kv_append(c.cache, c.batch, k, kvh * D, v, kvh * D, s)
+        fl.fl_kv_read(c.cache, c.batch, None, ko, kvh * D, vo, kvh * D, s)
+        fl.fl_attn_paged(c.cache, c.batch, None, d_q, w, heads, 0.1, 0, 0, d_out, w, ws, n, s)
+
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        calls()
+        st.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            calls()
+    for lens, news in (([300, 200, 100], [2, 60, 1]), ([310, 70, 384], [10, 64, 0]), ([0, 384, 1], [0, 1, 1])):
+        c.lens, c.news = lens, news
+        c.start = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        c.table = np.random.default_rng(sum(lens)).permutation(c.num_pages * 2)[:18].reshape(3, 6).astype(np.int32)
+        used = [(i, b) for i in range(3) for b in range(-(-lens[i] // 64))]
+        for x, (i, b) in enumerate(used):
+            c.table[i, b] = x % c.num_pages if len(used) <= c.num_pages else x
+        if len(used) > c.num_pages:
+            pytest.fail("the test's cache is too small")
+        c.d_table.copy_(torch.from_numpy(c.table))
+        c.d_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        c.d_start.copy_(torch.from_numpy(c.start))
+        d_out.fill_(77)
+        graph.replay()
+        fl.fl_device_status()
+        c.pages = c.d_pages.cpu().numpy()
+        got = d_out.cpu().numpy().view(np.uint16)
+        c.check(got, q, heads, 0.1)
+        c.untouched(got)
+    del graph
+
+
+def test_run_together_a_speculation_window(env):
+    """A prompt, then draft steps that read the cache at 4 bits and write their own keys, and one
+    verification call over the window at 8 bits, all on one cache, each against the reference."""
+    torch, fl = env
+    kvh, heads, D, prompt, K = 2, 4, 64, 137, 5
+    width = 4
+    c = Case(torch, fl, [prompt + K], [prompt], kvh, D, seed=12, width=width, rows=prompt, max_new=prompt)
+    g = np.random.default_rng(99)
+    w, kw = heads * D, kvh * D
+    four = torch.full((1, width), 2, dtype=torch.uint8, device="cuda")
+    allk, allv = (synth.bf16_normal((prompt + K, kvh, D), 12, x) for x in (1, 2))
+    allq = synth.bf16_normal((prompt + K, heads, D), 12, 3)
+    d_k, d_v, d_q = dev(torch, allk), dev(torch, allv), dev(torch, allq)
+    out = torch.zeros((prompt + K, heads, D), dtype=torch.int16, device="cuda")
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    nbytes = fl.fl_attn_workspace_bytes(1, heads, kvh, D, prompt)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+
+    def step(first, n, levels, append):
+        lens.fill_(first + n)
+        start = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        b = fl.kv_batch(c.d_table, lens, start, 1, width, n, n)
+        if append:
+            fl.fl_kv_append(c.cache, b, d_k[first:], kw, d_v[first:], kw)
+        fl.fl_attn_paged(c.cache, b, levels, d_q[first:], w, heads, 0.125, 0, 0, out[first:], w, ws, nbytes)
+        torch.cuda.synchronize()
+        return out[first:first + n].cpu().numpy().view(np.uint16).copy()
+
+    got = {"prompt": step(0, prompt, None, True)}
+    for t in range(K):
+        got[t] = step(prompt + t, 1, four, True)
+    got["verify"] = step(prompt, K, None, False)
+    fl.fl_device_status()
+    pages = c.d_pages.cpu().numpy()
+    for name, first, n, level in [("prompt", 0, prompt, 4), ("verify", prompt, K, 4)] + [(t, prompt + t, 1, 2) for t in range(K)]:
+        for h in range(kvh):
+            k, v, lv, sc = kv.gather(pages, c.table[0], [level] * width, first + n, D, h)
+            for x in (2 * h, 2 * h + 1):
+                ref, tol = kv.attention(f64(allq[first:first + n, x]), k, v, lv, sc, np.arange(first, first + n),
+                                        np.float32(0.125), 0, 0)
+                assert np.all(np.abs(f64(got[name][:, x]) - ref) <= tol), (name, x)
+    code, s = kv.quantise(f64(allk))
+    k, _, _, _ = kv.gather(pages, c.table[0], None, prompt + K, D, 1)
+    assert np.array_equal(k, s[:, 1, None].astype(np.float64) * code[:, 1])
+
+
+def test_many_sequences(env):
+    """1024 sequences, most of them empty or short; and lengths that leave most CTAs idle."""
+    torch, fl = env
+    g = np.random.default_rng(1)
+    lens = [int(x) for x in np.where(g.random(1024) < 0.7, 0, g.integers(1, 90, 1024))]
+    news = [min(1, n) for n in lens]
+    c = Case(torch, fl, lens, news, 1, 64, seed=77)
+    q = c.q(2)
+    c.check(c.attend(q, 2, 0.125), q, 2, 0.125)
+    fl.fl_device_status()
+
+
+def test_pages_beyond_32_bit_offsets(env):
+    """A cache of more than 2^32 bytes: tokens in its last pages are written, read and attended to."""
+    torch, fl = env
+    kvh, D = 8, 128
+    per = fl.fl_kv_page_bytes(kvh, D)
+    num = (1 << 32) // per + 40
+    pages = torch.empty(num * per, dtype=torch.uint8, device="cuda")
+    assert num * per > 1 << 32
+    table = torch.tensor([[num - 1, num - 17, 3]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([150], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 150], dtype=torch.int32, device="cuda")
+    cache, b = fl.kv_cache(pages, num, kvh, D), fl.kv_batch(table, lens, start, 1, 3, 150, 150)
+    k, v = synth.bf16_normal((150, kvh, D), 4, 1), synth.bf16_normal((150, kvh, D), 4, 2)
+    q = synth.bf16_normal((150, 16, D), 4, 3)
+    fl.fl_kv_append(cache, b, dev(torch, k), kvh * D, dev(torch, v), kvh * D)
+    ko, vo = torch.zeros((150, kvh, D), dtype=torch.int16, device="cuda"), torch.zeros((150, kvh, D), dtype=torch.int16, device="cuda")
+    fl.fl_kv_read(cache, b, None, ko, kvh * D, vo, kvh * D)
+    out = torch.zeros((150, 16, D), dtype=torch.int16, device="cuda")
+    n = fl.fl_attn_workspace_bytes(1, 16, kvh, D, 150)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    fl.fl_attn_paged(cache, b, None, dev(torch, q), 16 * D, 16, D ** -0.5, 0, 0, out, 16 * D, ws, n)
+    fl.fl_device_status()
+    (kc, ks), (vc, vs) = kv.quantise(f64(k)), kv.quantise(f64(v))
+    assert np.array_equal(ko.cpu().numpy().view(np.uint16), synth.f32_to_bf16_bits(ks[..., None] * kc.astype(np.float32)))
+    assert np.array_equal(vo.cpu().numpy().view(np.uint16), synth.f32_to_bf16_bits(vs[..., None] * vc.astype(np.float32)))
+    for h in (0, 7):
+        kk, vv = ks[:, h, None].astype(np.float64) * kc[:, h], vs[:, h, None].astype(np.float64) * vc[:, h]
+        sc = np.stack([ks[:, h], vs[:, h]])
+        for x in (2 * h, 2 * h + 1):
+            ref, tol = kv.attention(f64(q[:, x]), kk, vv, np.full(150, 4), sc, np.arange(150), np.float32(D ** -0.5), 0, 0)
+            assert np.all(np.abs(f64(out[:, x].cpu().numpy()) - ref) <= tol)

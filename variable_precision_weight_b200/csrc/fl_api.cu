@@ -75,6 +75,12 @@ int take_device_error();
 namespace tc {
 int take_device_error();
 }
+namespace kv {
+int take_device_error();
+}
+namespace attn {
+int take_device_error();
+}
 int take_gate_error();
 }  // namespace fl
 
@@ -82,9 +88,10 @@ extern "C" fl_status fl_device_status(void) {
   using namespace fl;
   FL_CHECK_CUDA(cudaDeviceSynchronize(), "fl_device_status: cudaDeviceSynchronize");
   const int g = gemv::take_device_error(), k = kq::take_device_error(), t = take_gate_error();
-  const int c = tc::take_device_error();
-  if (g < 0 || k < 0 || t < 0 || c < 0) return fail(FL_ERR_CUDA, "fl_device_status: reading the error words failed");
-  if (g == 0 && k == 0 && t == 0 && c == 0) return FL_OK;
+  const int c = tc::take_device_error(), v = kv::take_device_error(), at = attn::take_device_error();
+  if (g < 0 || k < 0 || t < 0 || c < 0 || v < 0 || at < 0)
+    return fail(FL_ERR_CUDA, "fl_device_status: reading the error words failed");
+  if (g == 0 && k == 0 && t == 0 && c == 0 && v == 0 && at == 0) return FL_OK;
   auto what = [](int c) {
     return c == 1 ? "a producer's wait for a free stage" : c == 2 ? "a consumer's wait for a full stage"
          : c == 3 ? "the wait for staged activations" : c == 4 ? "the self-test wait" : "a wait";
@@ -97,6 +104,13 @@ extern "C" fl_status fl_device_status(void) {
     const char* cw = c == 1 ? "the producer's wait for a free stage" : c == 2 ? "the MMA issuer's wait for codes or a free accumulator"
                    : c == 3 ? "a converter's wait for a full stage or a free code buffer" : "an epilogue wait for the MMAs";
     return fail(FL_ERR_TIMEOUT, "tensor-core GEMV: %s ran out (code %d); its outputs are not valid", cw, c);
+  }
+  if (at == 3) return fail(FL_ERR_TIMEOUT, "attention: a wait ran out; its outputs are not valid");
+  for (const auto& e : {std::make_pair(v, "cache append or read"), std::make_pair(at, "attention")}) {
+    if (e.first == 2)
+      return fail(FL_ERR_ARG, "%s: a page index was out of range; that block was left out", e.second);
+    if (e.first == 1)
+      return fail(FL_ERR_ARG, "%s: a sequence's length or rows contradict the batch; it was left out", e.second);
   }
   return fail(FL_ERR_TIMEOUT, "logit gate: the wait for the cluster's partials ran out; its outputs are NaN");
 }

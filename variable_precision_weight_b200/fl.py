@@ -72,10 +72,23 @@ class fl_decide_params(C.Structure):
                 ("counters", C.c_void_p)]
 
 
+class fl_kv_cache(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("num_pages", C.c_int), ("kv_heads", C.c_int), ("head_dim", C.c_int)]
+
+
+class fl_kv_batch(C.Structure):
+    _fields_ = [("block_table", C.c_void_p), ("lens", C.c_void_p), ("new_start", C.c_void_p), ("n_seqs", C.c_int),
+                ("max_blocks", C.c_int), ("rows", C.c_int), ("max_new", C.c_int)]
+
+
+FL_KV_BLOCK = 64
+FL_KV_MAX_SEQS = 1024
+FL_ATTN_MAX_GROUP = 32
+
 FL_DECIDE_LADDER = 0
 FL_DECIDE_SHARE = 1
 
-_P, _I, _F, _S = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+_P, _I, _F, _S, _L = C.c_void_p, C.c_int, C.c_float, C.c_size_t, C.c_int64
 _sigs = {
     "fl_status_string": (C.c_char_p, [_I]),
     "fl_last_error": (C.c_char_p, []),
@@ -107,6 +120,12 @@ _sigs = {
     "fl_shard_blocks": (_I, [_P, _I, _I, _I, _P]),
     "fl_logit_gate_partial": (_I, [_P, _I, _I, _I, _P, _P]),
     "fl_logit_gate_merge": (_I, [_P, _I, _I, _F, _F, _P, _P, _P, _P, _P]),
+    "fl_kv_page_bytes": (_S, [_I, _I]),
+    "fl_kv_append": (_I, [C.POINTER(fl_kv_cache), C.POINTER(fl_kv_batch), _P, _L, _P, _L, _P]),
+    "fl_kv_read": (_I, [C.POINTER(fl_kv_cache), C.POINTER(fl_kv_batch), _P, _P, _L, _P, _L, _P]),
+    "fl_attn_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "fl_attn_paged": (_I, [C.POINTER(fl_kv_cache), C.POINTER(fl_kv_batch), _P, _P, _L, _I, _F, _I, _I, _P, _L, _P, _S,
+                           _P]),
 }
 for _name, (_res, _args) in _sigs.items():
     _fn = getattr(_lib, _name)
@@ -345,3 +364,45 @@ def fl_logit_gate_merge(partials, nparts: int, batch: int, tau_h: float, tau_m: 
     """partials: device [nparts][batch] fl_gate_partial records (nparts * batch * 32 bytes)."""
     _check(_lib.fl_logit_gate_merge(_ptr(partials), nparts, batch, float(tau_h), float(tau_m), _ptr(entropy),
                                     _ptr(margin), _ptr(top2), _ptr(escalate), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- paged key/value cache, attention
+
+def fl_kv_page_bytes(kv_heads: int, head_dim: int) -> int:
+    return int(_lib.fl_kv_page_bytes(kv_heads, head_dim))
+
+
+def kv_cache(pages, num_pages: int, kv_heads: int, head_dim: int) -> fl_kv_cache:
+    """pages: a device buffer of num_pages * fl_kv_page_bytes(kv_heads, head_dim) bytes."""
+    return fl_kv_cache(_ptr(pages), num_pages, kv_heads, head_dim)
+
+
+def kv_batch(block_table, lens, new_start, n_seqs: int, max_blocks: int, rows: int, max_new: int) -> fl_kv_batch:
+    """Device int32 block_table [n_seqs, max_blocks], lens [n_seqs], new_start [n_seqs + 1] (or None:
+    one new token per sequence). The struct holds raw pointers: keep the tensors alive with it."""
+    return fl_kv_batch(_ptr(block_table), _ptr(lens), _ptr(new_start), n_seqs, max_blocks, rows, max_new)
+
+
+def fl_kv_append(cache: fl_kv_cache, batch: fl_kv_batch, k, k_stride: int, v, v_stride: int, stream=None) -> None:
+    """k, v: device bf16 [rows][kv_heads][head_dim], row strides in elements."""
+    _check(_lib.fl_kv_append(C.byref(cache), C.byref(batch), _ptr(k), k_stride, _ptr(v), v_stride, _stream(stream)))
+
+
+def fl_kv_read(cache: fl_kv_cache, batch: fl_kv_batch, levels, k, k_stride: int, v, v_stride: int,
+               stream=None) -> None:
+    """levels: device uint8 [n_seqs, max_blocks] or None (every block at eight bits)."""
+    _check(_lib.fl_kv_read(C.byref(cache), C.byref(batch), _ptr(levels), _ptr(k), k_stride, _ptr(v), v_stride,
+                           _stream(stream)))
+
+
+def fl_attn_workspace_bytes(n_seqs: int, heads: int, kv_heads: int, head_dim: int, max_new: int) -> int:
+    return int(_lib.fl_attn_workspace_bytes(n_seqs, heads, kv_heads, head_dim, max_new))
+
+
+def fl_attn_paged(cache: fl_kv_cache, batch: fl_kv_batch, levels, q, q_stride: int, heads: int, scale: float,
+                  window: int, sinks: int, out, out_stride: int, workspace, workspace_bytes: int,
+                  stream=None) -> None:
+    """q, out: device bf16 [rows][heads][head_dim], row strides in elements."""
+    _check(_lib.fl_attn_paged(C.byref(cache), C.byref(batch), _ptr(levels), _ptr(q), q_stride, heads, float(scale),
+                              window, sinks, _ptr(out), out_stride, _ptr(workspace), workspace_bytes,
+                              _stream(stream)))
