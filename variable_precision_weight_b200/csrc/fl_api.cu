@@ -81,6 +81,9 @@ int take_device_error();
 namespace attn {
 int take_device_error();
 }
+namespace attn_tc {
+int take_device_error();
+}
 int take_gate_error();
 }  // namespace fl
 
@@ -88,8 +91,9 @@ extern "C" fl_status fl_device_status(void) {
   using namespace fl;
   FL_CHECK_CUDA(cudaDeviceSynchronize(), "fl_device_status: cudaDeviceSynchronize");
   const int g = gemv::take_device_error(), k = kq::take_device_error(), t = take_gate_error();
-  const int c = tc::take_device_error(), v = kv::take_device_error(), at = attn::take_device_error();
-  if (g < 0 || k < 0 || t < 0 || c < 0 || v < 0 || at < 0)
+  const int c = tc::take_device_error(), v = kv::take_device_error(), a1 = attn::take_device_error();
+  const int a2 = attn_tc::take_device_error(), at = a1 > a2 ? a1 : a2;
+  if (g < 0 || k < 0 || t < 0 || c < 0 || v < 0 || a1 < 0 || a2 < 0)
     return fail(FL_ERR_CUDA, "fl_device_status: reading the error words failed");
   if (g == 0 && k == 0 && t == 0 && c == 0 && v == 0 && at == 0) return FL_OK;
   auto what = [](int c) {

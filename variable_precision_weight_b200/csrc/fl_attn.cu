@@ -62,30 +62,20 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ float lds32(const uint8_t* p) { return *reinterpret_cast<const float*>(p); }
-
 __device__ __forceinline__ void consumer_bar() { asm volatile("bar.sync 1, %0;" ::"r"(kConsumers) : "memory"); }
-
-__device__ __forceinline__ uint32_t atom_add_acq_rel(uint32_t* p, uint32_t v) {
-  uint32_t old;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
-}
 
 // A warp's state for one item: query columns 8 nt + 2 t and + 1 of lane (g, t).
 template <int D, int NT>
 struct State {
   float o[D / 16][NT][4];
-  float m[NT][2], l[NT][2], p4[NT][2];  // l and p4 are this lane's share of the keys
+  float m[NT][2], l[NT][2];  // l is this lane's share of the keys
 };
 
 // One page: scores of its 64 keys, the online softmax step, and the product with its values.
 // mask(key, pos) is applied only where the page is not wholly visible.
 template <int D, int NT, bool kD8>
 __device__ __forceinline__ void page_step(const Args& a, const uint8_t* rec, int key0, bool masked, const int (&pos)[NT][2],
-                                          const uint32_t (&qf)[D / 16][NT][2], const float (&q4)[NT][2],
-                                          State<D, NT>& st) {
+                                          const uint32_t (&qf)[D / 16][NT][2], State<D, NT>& st) {
   const int lane = threadIdx.x & 31, g = lane >> 2;
   const uint8_t* const khi = rec + kv::kScaleBytes + 16 * lane;
   const uint8_t* const klo = khi + 2 * kv::plane_bytes(D);
@@ -106,24 +96,25 @@ __device__ __forceinline__ void page_step(const Args& a, const uint8_t* rec, int
       uint4 l = make_uint4(0, 0, 0, 0);
       if (kD8) l = lds128(klo + off);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t hx = ks < 2 ? h.x : h.y, hz = ks < 2 ? h.z : h.w, lx = ks < 2 ? l.x : l.y,
-                       lz = ks < 2 ? l.z : l.w;
-        const int k = 2 * (ks & 1);
-        const uint32_t a0 = code_pair<kD8>(hx, lx, k), a1 = code_pair<kD8>(hz, lz, k);
-        const uint32_t a2 = code_pair<kD8>(hx, lx, k + 1), a3 = code_pair<kD8>(hz, lz, k + 1);
+      for (int w = 0; w < 2; ++w) {  // 8 dims of a lane's 16
+        uint32_t x[4], y[4];         // slots 4 s + .. and 4 s + 2 + ..
+        unpack_word<kD8>(w ? h.y : h.x, w ? l.y : l.x, x);
+        unpack_word<kD8>(w ? h.w : h.z, w ? l.w : l.z, y);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_bf16(z[s][nt], a0, a1, a2, a3, qf[4 * S + ks][nt][0], qf[4 * S + ks][nt][1]);
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_bf16(z[s][nt], x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1], qf[4 * S + 2 * w + e][nt][0],
+                     qf[4 * S + 2 * w + e][nt][1]);
       }
     }
-    const float k0 = lds32(rec + 4 * (slot0 + 4 * s)) * (kD8 ? a.scale_log2 : 16.f * a.scale_log2);
-    const float k1 = lds32(rec + 4 * (slot0 + 4 * s + 2)) * (kD8 ? a.scale_log2 : 16.f * a.scale_log2);
+    const float k0 = lds32(rec + 4 * (slot0 + 4 * s)) * (value_factor<kD8>() * a.scale_log2);
+    const float k1 = lds32(rec + 4 * (slot0 + 4 * s + 2)) * (value_factor<kD8>() * a.scale_log2);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        z[s][nt][c] = (kD8 ? z[s][nt][c] : z[s][nt][c] + q4[nt][c & 1]) * (c < 2 ? k0 : k1);
+        z[s][nt][c] *= c < 2 ? k0 : k1;
   }
   if (masked) {
 #pragma unroll
@@ -156,10 +147,7 @@ __device__ __forceinline__ void page_step(const Args& a, const uint8_t* rec, int
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        st.l[nt][e] *= alpha[nt][e];
-        st.p4[nt][e] *= alpha[nt][e];
-      }
+      for (int e = 0; e < 2; ++e) st.l[nt][e] *= alpha[nt][e];
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt)
 #pragma unroll
@@ -169,8 +157,8 @@ __device__ __forceinline__ void page_step(const Args& a, const uint8_t* rec, int
   uint32_t pf[4][NT][2];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const float v0 = lds32(rec + 256 + 4 * (slot0 + 4 * s)) * (kD8 ? 1.f : 16.f);
-    const float v1 = lds32(rec + 256 + 4 * (slot0 + 4 * s + 2)) * (kD8 ? 1.f : 16.f);
+    const float v0 = lds32(rec + 256 + 4 * (slot0 + 4 * s)) * value_factor<kD8>();
+    const float v1 = lds32(rec + 256 + 4 * (slot0 + 4 * s + 2)) * value_factor<kD8>();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float p[4];
@@ -180,7 +168,6 @@ __device__ __forceinline__ void page_step(const Args& a, const uint8_t* rec, int
         st.l[nt][c & 1] += e;
         // a key that is not seen has weight 0 whatever its value's scale is
         p[c] = masked && z[s][nt][c] == -INFINITY ? 0.f : e * (c < 2 ? v0 : v1);
-        if (!kD8) st.p4[nt][c & 1] += p[c];
       }
       pf[s][nt][0] = transpose8x8(bf16x2(p[0], p[1]));
       pf[s][nt][1] = transpose8x8(bf16x2(p[2], p[3]));
@@ -193,27 +180,12 @@ __device__ __forceinline__ void page_step(const Args& a, const uint8_t* rec, int
     if (kD8) l = lds128(vlo + 512 * dt);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const uint32_t hw = s == 0 ? h.x : s == 1 ? h.y : s == 2 ? h.z : h.w;
-      const uint32_t lw = s == 0 ? l.x : s == 1 ? l.y : s == 2 ? l.z : l.w;
-      const uint32_t a0 = code_pair<kD8>(hw, lw, 0), a1 = code_pair<kD8>(hw, lw, 1);
-      const uint32_t a2 = code_pair<kD8>(hw, lw, 2), a3 = code_pair<kD8>(hw, lw, 3);
+      uint32_t x[4];
+      unpack_word<kD8>(s == 0 ? h.x : s == 1 ? h.y : s == 2 ? h.z : h.w, s == 0 ? l.x : s == 1 ? l.y : s == 2 ? l.z : l.w, x);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_bf16(st.o[dt][nt], a0, a1, a2, a3, pf[s][nt][0], pf[s][nt][1]);
+      for (int nt = 0; nt < NT; ++nt) mma_bf16(st.o[dt][nt], x[0], x[1], x[2], x[3], pf[s][nt][0], pf[s][nt][1]);
     }
   }
-}
-
-// Sequence whose units hold u: the last i with pre[i] <= u (empty sequences are passed over).
-__device__ __forceinline__ int find_seq(const long long* pre, int n, long long u) {
-  int lo = 0, hi = n;  // pre[lo] <= u < pre[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= u)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
 }
 
 template <int D, int NT>
@@ -349,13 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 
     // query fragments: column n = 8 nt + g, dims 64 S + 16 t + 4 ks .. + 3
     uint32_t qf[D / 16][NT][2];
-    float q4[NT][2];
     int pos[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = min(8 * nt + g, nrows - 1) + r0;
       const uint16_t* qp = a.q + (int64_t)(geo.s.row0 + r / a.group) * a.q_stride + (head * a.group + r % a.group) * D;
-      float sum = 0.f;
 #pragma unroll
       for (int S = 0; S < D / 64; ++S) {
         const uint4 q0 = __ldg(reinterpret_cast<const uint4*>(qp + 64 * S + 16 * t));
@@ -366,15 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
           qf[4 * S + ks][nt][0] = w[2 * ks];
           qf[4 * S + ks][nt][1] = w[2 * ks + 1];
         }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) sum += __uint_as_float(w[x] << 16) + __uint_as_float(w[x] & 0xFFFF0000u);
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        // D4 values are 16 (h - 8 + 7.5 / 16): the constant's share of a score, per column
-        q4[nt][e] = 0.46875f * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
         pos[nt][e] = geo.pos0 + (min(8 * nt + 2 * t + e, nrows - 1) + r0) / a.group;
       }
     }
@@ -384,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         st.m[nt][e] = -INFINITY;
-        st.l[nt][e] = st.p4[nt][e] = 0.f;
+        st.l[nt][e] = 0.f;
       }
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt)
@@ -413,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       const bool masked = key1 > pos_lo || (a.window > 0 && pos_hi - key0 >= a.window && key1 >= a.sinks);
       if (!none) {
         if (mt.y == 4)
-          page_step<D, NT, true>(a, rec, key0, masked, pos, qf, q4, st);
+          page_step<D, NT, true>(a, rec, key0, masked, pos, qf, st);
         else
-          page_step<D, NT, false>(a, rec, key0, masked, pos, qf, q4, st);
+          page_step<D, NT, false>(a, rec, key0, masked, pos, qf, st);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty_bar[s]);
@@ -425,12 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float l = st.l[nt][e], p4 = st.p4[nt][e];
+        float l = st.l[nt][e];
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          l += __shfl_xor_sync(0xffffffffu, l, d);
-          p4 += __shfl_xor_sync(0xffffffffu, p4, d);
-        }
+        for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
         const int r = 8 * nt + 2 * t + e;
         if (g == 0) {
           sm_m[warp][r] = st.m[nt][e];
@@ -439,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         float* jp = join + (warp * R + r) * C::kPitch + g;
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) {
-          jp[16 * dt] = fmaf(0.46875f, p4, st.o[dt][nt][e]);
-          jp[16 * dt + 8] = fmaf(0.46875f, p4, st.o[dt][nt][e + 2]);
+          jp[16 * dt] = st.o[dt][nt][e];
+          jp[16 * dt + 8] = st.o[dt][nt][e + 2];
         }
       }
     consumer_bar();
@@ -523,18 +484,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 // ---------------------------------------------------------------- host side
 
 struct Ws {
-  size_t tickets, partial, total;
+  size_t tickets, tc_tickets, partial, tc_partial, total;
 };
+
+// Sequences with more rows (new tokens x group) than this take the tcgen05 kernel.
+constexpr int kSmallRows = 32;
 
 // Rows per tile by the largest number of rows a (sequence, head) has: eight columns cost half the
 // MMAs of sixteen.
-static int row_tiles(int max_rows) { return max_rows <= 8 ? 1 : 2; }
+static int row_tiles(long long max_rows) { return max_rows <= 8 ? 1 : 2; }
 
-static Ws ws_layout(int nsm, int D, int nt) {
+static Ws ws_layout(int nsm, int D, long long max_rows) {
   Ws w;
   w.tickets = 0;
-  w.partial = (size_t)kMaxGrid * 4;
-  w.total = w.partial + (size_t)nsm * 2 * (8 * nt) * (D + 2) * 4;
+  w.tc_tickets = (size_t)kMaxGrid * 4;
+  w.partial = 2 * (size_t)kMaxGrid * 4;
+  w.tc_partial = w.partial + (size_t)nsm * 2 * (8 * row_tiles(max_rows)) * (D + 2) * 4;
+  w.total = w.tc_partial + (max_rows > kSmallRows ? attn_tc::partial_bytes(D, nsm) : 0);
   return w;
 }
 
@@ -569,7 +535,7 @@ extern "C" size_t fl_attn_workspace_bytes(int n_seqs, int heads, int kv_heads, i
   using namespace fl;
   const int nsm = std::min(device_sm_count(), attn::kMaxGrid);
   if (nsm <= 0 || !attn::shape_ok(n_seqs, heads, kv_heads, head_dim, max_new)) return 0;
-  return attn::ws_layout(nsm, head_dim, attn::row_tiles(max_new * (heads / kv_heads))).total;
+  return attn::ws_layout(nsm, head_dim, (long long)max_new * (heads / kv_heads)).total;
 }
 
 extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* batch, const uint8_t* levels,
@@ -595,7 +561,7 @@ extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* 
   if (units > 2147483647.0 || units * batch->n_seqs / nsm > 2147483647.0)
     return fail(FL_ERR_SHAPE, "%s: max_new=%d over max_blocks=%d is too large for one call", what, batch->max_new,
                 batch->max_blocks);
-  const attn::Ws wl = attn::ws_layout(nsm, D, nt);
+  const attn::Ws wl = attn::ws_layout(nsm, D, max_rows);
   if (!workspace || workspace_bytes < wl.total)
     return fail(FL_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, workspace ? workspace_bytes : (size_t)0,
                 wl.total);
@@ -617,10 +583,16 @@ extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* 
   a.window = window;
   a.sinks = sinks;
   a.min_rows = 1;
-  a.max_rows = 0x7fffffff;
+  a.max_rows = attn::kSmallRows;
   a.tickets = reinterpret_cast<uint32_t*>(wsb + wl.tickets);
   a.partial = reinterpret_cast<float*>(wsb + wl.partial);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (D == 64) return nt == 1 ? attn::launch<64, 1>(a, nsm, st) : attn::launch<64, 2>(a, nsm, st);
-  return nt == 1 ? attn::launch<128, 1>(a, nsm, st) : attn::launch<128, 2>(a, nsm, st);
+  fl_status s = D == 64 ? (nt == 1 ? attn::launch<64, 1>(a, nsm, st) : attn::launch<64, 2>(a, nsm, st))
+                        : (nt == 1 ? attn::launch<128, 1>(a, nsm, st) : attn::launch<128, 2>(a, nsm, st));
+  if (s || max_rows <= attn::kSmallRows) return s;
+  a.min_rows = attn::kSmallRows + 1;
+  a.max_rows = 0x7fffffff;
+  a.tickets = reinterpret_cast<uint32_t*>(wsb + wl.tc_tickets);
+  a.partial = reinterpret_cast<float*>(wsb + wl.tc_partial);
+  return attn_tc::launch(a, D, nsm, st);
 }
