@@ -87,8 +87,8 @@ __device__ __forceinline__ void unpack_word(uint32_t hi, uint32_t lo, uint32_t (
     const uint32_t y = (hi & 0xF0F0F0F0u) | ((lo >> 4) & 0x0F0F0F0Fu);
     r[0] = fma_bf16x2(x & 0x00FF00FFu, 0x7E807E80u, 0xBF80BF80u);
     r[1] = fma_bf16x2(y & 0x00FF00FFu, 0x7E807E80u, 0xBF80BF80u);
-    r[2] = fma_bf16x2((x >> 8) & 0x00FF00FFu, 0x7E807E80u, 0xBF80BF80u);
-    r[3] = fma_bf16x2((y >> 8) & 0x00FF00FFu, 0x7E807E80u, 0xBF80BF80u);
+    r[2] = fma_bf16x2(__byte_perm(x, 0u, 0x4341), 0x7E807E80u, 0xBF80BF80u);
+    r[3] = fma_bf16x2(__byte_perm(y, 0u, 0x4341), 0x7E807E80u, 0xBF80BF80u);
   } else {
     const uint32_t w = hi >> 8;
     r[0] = fma_bf16x2(hi & 0x000F000Fu, 0x7F007F00u, 0xBDF1BDF1u);
@@ -96,6 +96,17 @@ __device__ __forceinline__ void unpack_word(uint32_t hi, uint32_t lo, uint32_t (
     r[2] = fma_bf16x2(w & 0x000F000Fu, 0x7F007F00u, 0xBDF1BDF1u);
     r[3] = fma_bf16x2(w & 0x00F000F0u, 0x7D007D00u, 0xBDF1BDF1u);
   }
+}
+
+// Wait on an mbarrier phase: polls that sleep up to a microsecond each, a bounded number of them
+// (about a second). Short on purpose: these kernels wait in many places, and their loops have to
+// stay in the instruction cache.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < (1 << 20); ++i)
+    if (mbar_try_sleep(a, parity, 1000)) return true;
+  return false;
 }
 
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }

@@ -39,10 +39,10 @@ using namespace attn;
 
 __device__ int g_error;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kTile = 128, kRows = 2 * kTile;  // rows of an MMA, of a unit
 constexpr int kStep = 2 * kv::kBlock;          // keys of a unit
-constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 4, kMmaWarp = 12, kLoadWarp = 13;
+constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 8, kMmaWarp = 16, kLoadWarp = 17;
 constexpr int kScaleRing = 4;  // steps whose scales are held; the operand ring keeps fewer in flight
 constexpr float kSlack = 8.f;  // a row's maximum moves when it grows by more than this (log2)
 
@@ -54,7 +54,7 @@ struct Cfg {
   static constexpr int kUnit = kv::kScaleBytes + 64 * D;  // a page's keys or values: both planes
   static constexpr int kRaw = D == 128 ? 6 : 8;
   static constexpr int kSmem = 1024 + kQ + kSlots * kSlotBytes + kRaw * kUnit;
-  static constexpr int kPiece = kRows * (D + 2);  // floats of a partial: o as [D/4][row][4], then (m, l) per row
+  static constexpr int kPiece = kRows * (D + 2);  // floats of a partial: o by row, then (m, l) per row
 };
 
 // ---------------------------------------------------------------- tcgen05
@@ -64,26 +64,21 @@ __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+// Tensor memory as mma fragments: 16 lanes by 8 columns per four registers, lane (g, t) holding
+// columns 2 t and 2 t + 1 of rows g (registers 0, 1) and g + 8 (2, 3); 16 registers are 32 columns.
+__device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+               : "r"(taddr));
 }
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_st_frag32(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+               : "memory");
+}
+// Packed pairs of such columns: four 32-bit columns per two registers (rows g and g + 8).
+__device__ __forceinline__ void tmem_st_pairs16(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Shared-memory matrix descriptor, K-major, 128-byte swizzle: rows of 128 bytes (64 bf16 of K) whose
@@ -100,6 +95,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n\t"
@@ -120,28 +120,30 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 
 // ---------------------------------------------------------------- pairs of fp32
-struct f2 {
-  uint64_t v;
-};
-__device__ __forceinline__ f2 pack2(float x, float y) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+// One instruction each; a value that enters every pair (twice) is made once, by a volatile move.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
   return r;
 }
-__device__ __forceinline__ void unpack2(f2 p, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.v)); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+__device__ __forceinline__ float2 unpack2(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
   return r;
 }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 
@@ -222,6 +224,197 @@ struct Walk {
   }
 };
 
+// ---------------------------------------------------------------- softmax of a step
+
+// What a lane's four rows see of a half step's columns: keys up to their position, and of those
+// the ones in the window or among the first; nothing where the page is not there.
+struct Sight {
+  int hi[4], lo[4], sink;  // relative to the half step's first key
+  __device__ __forceinline__ bool operator()(int r, int x) const { return x <= hi[r] && (x >= lo[r] || x < sink); }
+};
+__device__ __forceinline__ Sight sight_of(const Args& a, bool there, const int (&pos)[4], int key0) {
+  Sight s;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    s.hi[r] = there ? pos[r] - key0 : -1;
+    s.lo[r] = a.window > 0 ? max(pos[r] - a.window + 1, 0) - key0 : -key0;
+  }
+  s.sink = a.sinks - key0;
+  return s;
+}
+
+// Both passes over a step read S from tensor memory, 32 columns at a time, the next ones on their
+// way while these are worked on. Lane (g, t) holds rows 8 r + g of the warp's 32, columns 8 j + 2 t
+// and + 1: it needs a quarter of the columns' scales, and four rows share each. (S held in registers
+// over both passes took 1.1 times as long: its unrolled code outgrew the instruction cache.)
+struct Chunk {
+  uint32_t v[2][16];
+  __device__ __forceinline__ void load(uint32_t ts) {
+    tmem_ld_frag32(ts, v[0]);
+    tmem_ld_frag32(ts + (16u << 16), v[1]);
+  }
+  __device__ __forceinline__ uint64_t pair(int r, int j) const {
+    const uint32_t* const p = &v[r >> 1][4 * j + 2 * (r & 1)];
+    return pack2(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+};
+__device__ __forceinline__ void load_scales(uint64_t (&k)[4], const float* ks) {
+  const int t = threadIdx.x & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const uint64_t*>(ks + 8 * j + 2 * t);
+}
+
+// Each row's maximum over the scaled scores of 32 columns.
+template <bool kMasked>
+__device__ __forceinline__ void chunk_max(const Chunk& c, const uint64_t (&k)[4], const Sight& see, int x0, float (&mx)[4]) {
+  const int t = threadIdx.x & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float2 z = unpack2(mul2(c.pair(r, j), k[j]));
+      if (kMasked) {
+        z.x = see(r, x0 + 8 * j + 2 * t) ? z.x : -INFINITY;
+        z.y = see(r, x0 + 8 * j + 2 * t + 1) ? z.y : -INFINITY;
+      }
+      mx[r] = fmaxf(mx[r], fmaxf(z.x, z.y));
+    }
+}
+
+// P of 32 columns: 2^(z - m) times the value's scale, bf16, stored at tp; adds the powers to l. A
+// key that is not seen has weight 0 whatever its value's scale is.
+template <bool kMasked>
+__device__ __forceinline__ void chunk_probs(const Chunk& c, uint32_t tp, const uint64_t (&k)[4], const uint64_t (&v)[4],
+                                            const Sight& see, int x0, const uint64_t (&mneg)[4], float (&l)[4]) {
+  const int t = threadIdx.x & 3;
+  uint32_t pr[2][8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float2 z = unpack2(fma2(c.pair(r, j), k[j], mneg[r]));
+      if (kMasked) {
+        z.x = see(r, x0 + 8 * j + 2 * t) ? z.x : -INFINITY;
+        z.y = see(r, x0 + 8 * j + 2 * t + 1) ? z.y : -INFINITY;
+      }
+      const float ex = exp2_approx(z.x), ey = exp2_approx(z.y);
+      l[r] += ex + ey;
+      float2 w = unpack2(mul2(pack2(ex, ey), v[j]));
+      if (kMasked) {
+        w.x = see(r, x0 + 8 * j + 2 * t) ? w.x : 0.f;
+        w.y = see(r, x0 + 8 * j + 2 * t + 1) ? w.y : 0.f;
+      }
+      pr[r >> 1][2 * j + (r & 1)] = bf16x2(w.x, w.y);
+    }
+  tmem_st_pairs16(tp, pr[0]);
+  tmem_st_pairs16(tp + (16u << 16), pr[1]);
+}
+
+template <bool kMasked>
+__device__ __forceinline__ void step_max(const Args& a, uint32_t ts, const float* ks, const int* alive, const int (&pos)[4],
+                                         int key0, float (&mx)[4]) {
+  Chunk c[2];
+  c[0].load(ts);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const Sight see = kMasked ? sight_of(a, alive[h], pos, key0 + kv::kBlock * h) : Sight();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint64_t k[4];
+      load_scales(k, ks + 64 * h + 32 * e);
+      wait_ld();
+      if (e == 0 || h == 0) c[1 - e].load(ts + 64 * h + 32 * e + 32);
+      chunk_max<kMasked>(c[e], k, see, 32 * e, mx);
+    }
+  }
+}
+
+// P over S: keys 64 h .. of P take the columns 32 h .., read before. Arrives at bar[h] when they are stored.
+template <bool kMasked>
+__device__ __forceinline__ void step_probs(const Args& a, uint32_t ts, const float* ks, const float* vs, const int* alive,
+                                           const int (&pos)[4], int key0, const uint64_t (&mneg)[4], float (&l)[4],
+                                           uint64_t* bar) {
+  Chunk c[2];
+  c[0].load(ts);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    const Sight see = kMasked ? sight_of(a, alive[h], pos, key0 + kv::kBlock * h) : Sight();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint64_t k[4], v[4];
+      load_scales(k, ks + 64 * h + 32 * e);
+      load_scales(v, vs + 64 * h + 32 * e);
+      wait_ld();
+      if (e == 0 || h == 0) c[1 - e].load(ts + 64 * h + 32 * e + 32);
+      chunk_probs<kMasked>(c[e], ts + 32 * h + 16 * e, k, v, see, 32 * e, mneg, l);
+    }
+    wait_st();
+    fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar + h);
+  }
+}
+
+// Joins the pieces of a tile that CTAs c0 .. c1 left, in that order: a warp per row, four rows at a
+// time so that enough loads are in flight.
+template <int D>
+__device__ __forceinline__ void merge_rows(const Args& a, const Walk& w, int c0, int c1, int G, long long U) {
+  using C = Cfg<D>;
+  constexpr int kE = D / 32, kB = 4;  // elements of a lane, rows at a time
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r0 = warp; r0 < w.t.nrows; r0 += kB * kSoftWarps) {
+    float m[kB], l[kB], o[kB][kE];
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+      m[b] = -INFINITY;
+      l[b] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[b][e] = 0.f;
+    }
+#pragma unroll 2
+    for (int c = c0; c <= c1; ++c) {
+      // the tile's piece is its CTA's first unless the tile begins inside that CTA's range
+      const float* pp = a.partial + (size_t)(2 * c + (U * c / G < w.ia)) * C::kPiece;
+      float v[kB][kE];
+      float2 ml[kB];
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        const int r = min(r0 + b * kSoftWarps, w.t.nrows - 1);
+        ml[b] = __ldcg(reinterpret_cast<const float2*>(pp + kRows * D + 2 * r));
+        if (kE == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(pp + r * D + 4 * lane));
+          v[b][0] = x.x, v[b][1] = x.y, v[b][kE - 2] = x.z, v[b][kE - 1] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(pp + r * D + 2 * lane));
+          v[b][0] = x.x, v[b][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        const float mn = fmaxf(m[b], ml[b].x), mu = mn == -INFINITY ? 0.f : mn;
+        const float f0 = exp2_approx(m[b] - mu), f1 = exp2_approx(ml[b].x - mu);
+        m[b] = mn;
+        l[b] = fmaf(f1, ml[b].y, f0 * l[b]);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[b][e] = fmaf(f1, v[b][e], f0 * o[b][e]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+      const int r = r0 + b * kSoftWarps, rr = w.t.r0 + r;
+      if (r >= w.t.nrows) break;
+      const float inv = l[b] == 0.f ? 0.f : 1.f / l[b];
+      uint16_t* const op = a.out + (int64_t)(w.g.s.row0 + rr / a.group) * a.out_stride +
+                           (w.head * a.group + rr % a.group) * D + kE * lane;
+      const uint32_t lo = bf16x2(o[b][0] * inv, o[b][1] * inv);
+      if (kE == 4)
+        *reinterpret_cast<uint2*>(op) = make_uint2(lo, bf16x2(o[b][kE - 2] * inv, o[b][kE - 1] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(op) = lo;
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ Args a) {
   using C = Cfg<D>;
@@ -235,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   __shared__ long long pre[FL_KV_MAX_SEQS + 1];
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
+  __shared__ Walk walks[kLoadWarp + 1];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* const q_smem = smem;
   uint8_t* const op_smem = smem + C::kQ;
@@ -313,9 +507,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   fence_after();
   const uint32_t tmem = s_tmem;  // columns: S of either half at 0 and 128, O at 256 and 256 + D
 
-  Walk w;
-  if (warp <= kLoadWarp) w.seek(a, pre, u0);
+  // each warp's place lies in shared memory: it is read at a tile's ends only
+  Walk& w = walks[min(warp, kLoadWarp)];
+  if (warp <= kLoadWarp) {
+    Walk x;
+    x.seek(a, pre, u0);
+    if (lane == 0) w = x;
+    __syncwarp();
+  }
+  auto advance = [&] {
+    Walk x = w;
+    x.next(a, pre);
+    __syncwarp();
+    if (lane == 0) w = x;
+    __syncwarp();
+  };
 
+  // The launch's registers (640 x 96) by role: 8 warps x 128, 8 x 72, 4 x 80.
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- pages -> raw ring
     int unit = 0;
@@ -323,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     auto emit = [&](const uint8_t* src, int lv, bool values) {
       const int s = unit % NR;
       if (failed) return;
-      if (unit >= NR && !__all_sync(0xffffffffu, mbar_wait(&raw_empty[s], (uint32_t)((unit / NR - 1) & 1)))) {
+      if (unit >= NR && !__all_sync(0xffffffffu, ring_wait(&raw_empty[s], (uint32_t)((unit / NR - 1) & 1)))) {
         failed = true;
         return;
       }
@@ -348,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const int blocks = w.g.s.len / kv::kBlock + (w.g.s.len % kv::kBlock != 0);
       const uint8_t *src = nullptr, *prev_src[2] = {nullptr, nullptr};
       int lv = 0, prev_lv[2] = {0, 0};
-      for (int p = p0; p < p1 && !failed; ++p) {
+      for (int p = p0; p <= p1 && !failed; ++p) {  // keys of step p, values of the step before
         const int k = (p - p0) & 15;
         if (k == 0) {  // sixteen steps' table entries at once, two lanes per step
           lv = 0;
@@ -376,198 +586,177 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), 2 * k + e));
           cur_lv[e] = __shfl_sync(0xffffffffu, lv, 2 * k + e);
         }
-        emit(cur_src[0], cur_lv[0], false);
-        emit(cur_src[1], cur_lv[1], false);
-        if (p > p0) {
-          emit(prev_src[0], prev_lv[0], true);
-          emit(prev_src[1], prev_lv[1], true);
-        }
+#pragma unroll 1
+        for (int e = p < p1 ? 0 : 2; e < (p > p0 ? 4 : 2); ++e)
+          emit(e == 0 ? cur_src[0] : e == 1 ? cur_src[1] : e == 2 ? prev_src[0] : prev_src[1],
+               e == 0 ? cur_lv[0] : e == 1 ? cur_lv[1] : e == 2 ? prev_lv[0] : prev_lv[1], e >= 2);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           prev_src[e] = cur_src[e];
           prev_lv[e] = cur_lv[e];
         }
       }
-      emit(prev_src[0], prev_lv[0], true);
-      emit(prev_src[1], prev_lv[1], true);
       u = ue;
-      if (u < u1) w.next(a, pre);
+      if (u < u1) advance();
     }
     if (failed && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
     // no copy may still be landing when the CTA exits
     for (int k = max(0, unit - NR); k < unit; ++k)
-      if (!mbar_wait(&raw_full[k % NR], (uint32_t)((k / NR) & 1)) && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
-  } else if (warp >= kConvWarp && warp < kConvWarp + kConvWarps) {
-    // ---------------------------------------------------------------- raw ring -> operands
-    const int cw = warp - kConvWarp, g = lane >> 2, t = lane & 3;
-    int unit = 0, op = 0, step = 0;
-    bool failed = false;
-    auto convert = [&](bool values) {
-      const int os = op % NS;
-      if (failed) return;
-      if (op >= NS && !__all_sync(0xffffffffu, mbar_wait(&op_empty[os], (uint32_t)((op / NS - 1) & 1)))) {
-        failed = true;
-        return;
-      }
-      uint8_t* const dst = op_smem + os * C::kSlotBytes;
-#pragma unroll 1
-      for (int pg = 0; pg < 2; ++pg, ++unit) {
-        const int s = unit % NR;
-        if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[s], (uint32_t)((unit / NR) & 1)))) {
-          failed = true;
-          return;
-        }
-        const int lv = meta[s];
-        const uint8_t* const raw = raw_smem + s * C::kUnit;
-        if (!values) {  // 16 keys' scales per warp: lanes 0-15 keys, 16-31 values
-          const int x = 16 * cw + (lane & 15);
-          const float f = lv == 4 ? value_factor<true>() : value_factor<false>();
-          const float sc = lv > 0 ? lds32(raw + 256 * (lane >> 4) + 4 * x) * (lane < 16 ? f * a.scale_log2 : f) : 0.f;
-          (lane < 16 ? ksc : vsc)[step % kScaleRing][kv::kBlock * pg + x] = sc;
-          if (cw == 0 && lane == 0) alive[step % kScaleRing][pg] = lv > 0;
-        }
-#pragma unroll
-        for (int bb = 0; bb < D / 64; ++bb) {
-          const int b = D / 64 * cw + bb;  // 512 bytes of a plane
-          uint32_t r[4][4];
-          if (lv == 0) {  // a block that nobody sees: P is 0 there, the operand must be finite
-#pragma unroll
-            for (int x = 0; x < 16; ++x) r[x >> 2][x & 3] = 0u;
-          } else {
-            const uint4 h = lds128(raw + kv::kScaleBytes + 512 * b + 16 * lane);
-            if (lv == 4) {
-              const uint4 l = lds128(raw + kv::kScaleBytes + kv::plane_bytes(D) + 512 * b + 16 * lane);
-              unpack_word<true>(h.x, l.x, r[0]);
-              unpack_word<true>(h.y, l.y, r[1]);
-              unpack_word<true>(h.z, l.z, r[2]);
-              unpack_word<true>(h.w, l.w, r[3]);
-            } else {
-              unpack_word<false>(h.x, 0u, r[0]);
-              unpack_word<false>(h.y, 0u, r[1]);
-              unpack_word<false>(h.z, 0u, r[2]);
-              unpack_word<false>(h.w, 0u, r[3]);
-            }
-          }
-          if (!values) {  // words x, y: dims 16 t .. + 15 of a slot, z, w: of the slot two on
-            const int s4 = b / (D / 64), S = b % (D / 64);
-            const uint32_t row = (uint32_t)(kv::kBlock * pg + 16 * (g >> 1) + 4 * s4 + (g & 1));
-            uint8_t* const d = dst + S * (kStep * 128);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              *reinterpret_cast<uint4*>(d + sw128(row + 2 * (x >> 1), 2 * t + (x & 1))) =
-                  make_uint4(r[x][0], r[x][1], r[x][2], r[x][3]);
-          } else {  // dims 16 b + g (pairs 0, 2) and + 8 (pairs 1, 3), slots 16 t + 4 x ..
-            uint8_t* const d = dst + pg * (D * 128);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int x = 0; x < 2; ++x)
-                *reinterpret_cast<uint4*>(d + sw128((uint32_t)(16 * b + g + 8 * e), 2 * t + x)) =
-                    make_uint4(r[2 * x][e], r[2 * x][e + 2], r[2 * x + 1][e], r[2 * x + 1][e + 2]);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[s]);
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&op_full[os]);
-        if (!values) mbar_arrive(&sc_full[step % kScaleRing]);
-      }
-      if (!values) ++step;
-      ++op;
-    };
-    for (long long u = u0; u < u1 && !failed;) {
-      const long long ue = min(u1, w.ia + w.t.n);
-      const int n = (int)(ue - u);
-      for (int j = 0; j < n; ++j) {
-        convert(false);
-        if (j > 0) convert(true);
-      }
-      convert(true);
-      u = ue;
-      if (u < u1) w.next(a, pre);
-    }
-    if (failed && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+      if (!ring_wait(&raw_full[k % NR], (uint32_t)((k / NR) & 1)) && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
   } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issue
-    {
-      const uint32_t q_addr = smem_u32(q_smem), op_addr = smem_u32(op_smem);
+    // ---------------------------------------------------------------- MMA issue: one thread
+    if (elect_one()) {
+      const uint64_t q_desc = sw128_desc(smem_u32(q_smem)), op_desc = sw128_desc(smem_u32(op_smem));
       bool ok = true;
-      int base = 0;                     // operands before the piece
-      int nq[2] = {0, 0}, np[2] = {0, 0};
-      auto wait = [&](uint64_t* bar, int phase) { ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1))); };
-      auto op_wait = [&](int o) { wait(&op_full[o % NS], o / NS); };
+      int base = 0;               // operands before the piece
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+      auto op_wait = [&](int o) { ok = ok && ring_wait(&op_full[o % NS], (uint32_t)((o / NS) & 1)); };
       auto scores = [&](int t, int o) {
-        if (lane == 0) {
-          const uint32_t k_addr = op_addr + (uint32_t)(o % NS) * C::kSlotBytes;
-          fence_after();
+        const uint64_t qd = q_desc + (uint64_t)(t * (kTile * D * 2 / 16)), kd = op_desc + (uint64_t)((o % NS) * (C::kSlotBytes / 16));
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (uint32_t)(ks / 4) * (kTile * 128) + 32u * (ks % 4);
-            mma_ss(tmem + 128u * t, sw128_desc(q_addr + t * (kTile * D * 2) + off), sw128_desc(k_addr + off),
-                   idesc_bf16(kStep), ks > 0);
-          }
-          mma_commit(&s_full[t]);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t off = (uint64_t)((ks / 4) * (kTile * 128 / 16) + 2 * (ks % 4));
+          mma_ss(tmem + 128u * t, qd + off, kd + off, idesc_bf16(kStep), ks > 0);
         }
+        mma_commit(&s_full[t]);
       };
       for (long long u = u0; u < u1 && ok;) {
         const long long ue = min(u1, w.ia + w.t.n);
         const int n = (int)(ue - u), nt = w.t.nrows > kTile ? 2 : 1;
         op_wait(base);
         for (int t = 0; t < nt && ok; ++t) {
-          wait(&q_full[t], nq[t]++);
+          ok = ring_wait(&q_full[t], nq[t]++ & 1u);
+          fence_after();
           if (ok) scores(t, base);
         }
-        if (ok && lane == 0) mma_commit(&op_empty[base % NS]);
+        if (ok) mma_commit(&op_empty[base % NS]);
         for (int j = 0; j < n && ok; ++j) {
           const int vo = base + (j == n - 1 ? 2 * n - 1 : 2 * j + 2), ko = base + 2 * j + 1;
           op_wait(vo);
           if (j + 1 < n) op_wait(ko);
           for (int t = 0; t < nt && ok; ++t) {
-            const uint32_t v_addr = op_addr + (uint32_t)(vo % NS) * C::kSlotBytes;
+            const uint64_t vd = op_desc + (uint64_t)((vo % NS) * (C::kSlotBytes / 16));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              wait(&p_full[t][h], np[t]);
-              if (ok && lane == 0) {
-                fence_after();
+              ok = ok && ring_wait(&p_full[t][h], np[t] & 1u);
+              if (!ok) break;
+              fence_after();
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  mma_ts(tmem + 256u + (uint32_t)(D * t), tmem + 128u * t + 32u * h + 8u * ks,
-                         sw128_desc(v_addr + (uint32_t)(h * D * 128) + 32u * ks), idesc_bf16(D), j > 0 || h > 0 || ks > 0);
-              }
+              for (int ks = 0; ks < 4; ++ks)
+                mma_ts(tmem + 256u + (uint32_t)(D * t), tmem + 128u * t + 32u * h + 8u * ks,
+                       vd + (uint64_t)(h * (D * 128 / 16) + 2 * ks), idesc_bf16(D), j > 0 || h > 0 || ks > 0);
             }
             ++np[t];
             if (!ok) break;
-            if (lane == 0) {
-              if (t == nt - 1) mma_commit(&op_empty[vo % NS]);
-              if (j == n - 1) mma_commit(&o_full[t]);
-            }
+            if (t == nt - 1) mma_commit(&op_empty[vo % NS]);
+            if (j == n - 1) mma_commit(&o_full[t]);
             if (j + 1 < n) {
               scores(t, ko);
-              if (t == nt - 1 && lane == 0) mma_commit(&op_empty[ko % NS]);
+              if (t == nt - 1) mma_commit(&op_empty[ko % NS]);
             }
-            __syncwarp();
           }
         }
         base += 2 * n;
         u = ue;
         if (u < u1) w.next(a, pre);
       }
-      if (!ok && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
       // every MMA is complete before TMEM is freed: the last commit tracks all of them
-      if (ok && base > 0) {
-        const int o = base - 1;
-        wait(&op_empty[o % NS], o / NS);
-        if (!ok && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
-      }
+      if (ok && base > 0) ok = ring_wait(&op_empty[(base - 1) % NS], (uint32_t)(((base - 1) / NS) & 1));
+      if (!ok) atomicMax(&g_error, (int)kv::kErrWait);
     }
     __syncwarp();
-  } else if (warp < kSoftWarps) {
+  }
+  } else if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // ---------------------------------------------------------------- raw ring -> operands
+    // in the order K0, K1, V0, K2, V1, .., V(n - 1) of each piece
+    {
+      const int cw = warp - kConvWarp, g = lane >> 2, t = lane & 3;
+      int unit = 0, op = 0, step = 0;
+      bool failed = false;
+      for (long long u = u0; u < u1 && !failed;) {
+        const long long ue = min(u1, w.ia + w.t.n);
+        const int n = (int)(ue - u);
+#pragma unroll 1
+        for (int o = 0; o < 2 * n && !failed; ++o, ++op) {
+          const bool values = o == 2 * n - 1 || (o > 0 && o % 2 == 0);
+          const int os = op % NS, sr = step % kScaleRing;
+          failed = op >= NS && !__all_sync(0xffffffffu, ring_wait(&op_empty[os], (uint32_t)((op / NS - 1) & 1)));
+          uint8_t* const dst = op_smem + os * C::kSlotBytes;
+#pragma unroll 1
+          for (int pg = 0; pg < 2 && !failed; ++pg, ++unit) {
+            const int s = unit % NR;
+            if (!__all_sync(0xffffffffu, ring_wait(&raw_full[s], (uint32_t)((unit / NR) & 1)))) {
+              failed = true;
+              break;
+            }
+            const int lv = meta[s];
+            const uint8_t* const raw = raw_smem + s * C::kUnit;
+            if (!values && lane < 16) {  // 16 of the page's 64 keys' and 64 values' scales per warp
+              const int x = 16 * (cw & 3) + lane;
+              const float f = lv == 4 ? value_factor<true>() : value_factor<false>();
+              const float sc = lv > 0 ? lds32(raw + 64 * cw + 4 * lane) * (cw < 4 ? f * a.scale_log2 : f) : 0.f;
+              (cw < 4 ? ksc : vsc)[sr][kv::kBlock * pg + x] = sc;
+              if (cw == 0 && lane == 0) alive[sr][pg] = lv > 0;
+            }
+            // 512 bytes of a plane per warp: at D = 64, with four such blocks, four warps per page
+            if (D == 128 || (cw >> 2) == pg) {
+              const int b = D == 128 ? cw : cw & 3;
+              uint32_t r[4][4];
+              uint4 h = make_uint4(0, 0, 0, 0);  // a block that nobody sees: P is 0 there, but the operand must be finite
+              if (lv > 0) h = lds128(raw + kv::kScaleBytes + 512 * b + 16 * lane);
+              if (lv == 4) {
+                const uint4 l = lds128(raw + kv::kScaleBytes + kv::plane_bytes(D) + 512 * b + 16 * lane);
+                unpack_word<true>(h.x, l.x, r[0]);
+                unpack_word<true>(h.y, l.y, r[1]);
+                unpack_word<true>(h.z, l.z, r[2]);
+                unpack_word<true>(h.w, l.w, r[3]);
+              } else {
+                unpack_word<false>(h.x, 0u, r[0]);
+                unpack_word<false>(h.y, 0u, r[1]);
+                unpack_word<false>(h.z, 0u, r[2]);
+                unpack_word<false>(h.w, 0u, r[3]);
+              }
+              if (!values) {  // words x, y: dims 16 t .. + 15 of a slot, z, w: of the slot two on
+                const int s4 = b / (D / 64), S = b % (D / 64);
+                const uint32_t row = (uint32_t)(kv::kBlock * pg + 16 * (g >> 1) + 4 * s4 + (g & 1));
+                uint8_t* const d = dst + S * (kStep * 128);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  *reinterpret_cast<uint4*>(d + sw128(row + 2 * (x >> 1), 2 * t + (x & 1))) =
+                      make_uint4(r[x][0], r[x][1], r[x][2], r[x][3]);
+              } else {  // dims 16 b + g (pairs 0, 2) and + 8 (pairs 1, 3), slots 16 t + 4 x ..
+                uint8_t* const d = dst + pg * (D * 128);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                  for (int x = 0; x < 2; ++x)
+                    *reinterpret_cast<uint4*>(d + sw128((uint32_t)(16 * b + g + 8 * e), 2 * t + x)) =
+                        make_uint4(r[2 * x][e], r[2 * x][e + 2], r[2 * x + 1][e], r[2 * x + 1][e + 2]);
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_empty[s]);
+          }
+          if (failed) break;
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&op_full[os]);
+            if (!values) mbar_arrive(&sc_full[sr]);
+          }
+          if (!values) ++step;
+        }
+        u = ue;
+        if (u < u1) advance();
+      }
+      if (failed && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     // ---------------------------------------------------------------- softmax, epilogue
-    const int t = warp >> 2, row = 32 * (warp & 3) + lane;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const int t = warp >> 2, row = 32 * (warp & 3) + lane, fg = lane >> 2, ft = lane & 3;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, half = 16u << 16;
     const uint32_t ts = tmem + lanes + 128u * t, to = tmem + lanes + 256u + (uint32_t)(D * t);
     uint8_t* const qs = q_smem + t * (kTile * D * 2);
     int step = 0, cnt = 0, pieces = 0;  // steps of the CTA, of this half, pieces of this half
@@ -577,162 +766,127 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const int p0 = (int)(u - w.ia), n = (int)(ue - u);
       const bool live = w.t.nrows > kTile * t;  // this half has rows
       const bool whole = p0 == 0 && n == w.t.n;
-      float m = -INFINITY, l = 0.f;
       if (live && ok) {
-        const int rr = w.t.r0 + min(kTile * t + row, w.t.nrows - 1), pos = w.g.pos0 + rr / a.group;
-        const int plo = w.g.pos0 + (w.t.r0 + kTile * t) / a.group;
-        const int phi = w.g.pos0 + (w.t.r0 + min(kTile * t + kTile, w.t.nrows) - 1) / a.group;
-        const uint4* qp = reinterpret_cast<const uint4*>(a.q + (int64_t)(w.g.s.row0 + rr / a.group) * a.q_stride +
-                                                         (w.head * a.group + rr % a.group) * D);
+        {
+          const int rr = w.t.r0 + min(kTile * t + row, w.t.nrows - 1);
+          const uint4* qp = reinterpret_cast<const uint4*>(a.q + (int64_t)(w.g.s.row0 + rr / a.group) * a.q_stride +
+                                                           (w.head * a.group + rr % a.group) * D);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(qs + (c >> 3) * (kTile * 128) + sw128(row, c & 7)) = __ldg(qp + c);
+          for (int c = 0; c < D / 8; ++c)
+            *reinterpret_cast<uint4*>(qs + (c >> 3) * (kTile * 128) + sw128(row, c & 7)) = __ldg(qp + c);
+        }
         fence_async_smem();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
+        const int wr = kTile * t + 32 * (warp & 3) + fg;  // rows of this lane in the tile: wr + 8 r
+        int pos[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pos[r] = w.g.pos0 + (w.t.r0 + min(wr + 8 * r, w.t.nrows - 1)) / a.group;
+        const int plo = w.g.pos0 + (w.t.r0 + kTile * t) / a.group;
+        const int phi = w.g.pos0 + (w.t.r0 + min(kTile * t + kTile, w.t.nrows) - 1) / a.group;
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float l[4] = {0.f, 0.f, 0.f, 0.f};
         for (int j = 0; j < n && ok; ++j, ++cnt) {
           const int sr = (step + j) % kScaleRing, key0 = kStep * step_at(w.t, p0 + j);
-          ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[sr], (uint32_t)(((step + j) / kScaleRing) & 1)) &&
-                                           mbar_wait(&s_full[t], (uint32_t)(cnt & 1)));
+          ok = __all_sync(0xffffffffu, ring_wait(&sc_full[sr], (uint32_t)(((step + j) / kScaleRing) & 1)) &&
+                                           ring_wait(&s_full[t], (uint32_t)(cnt & 1)));
           if (!ok) break;
           fence_after();
-          bool masked[2];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          bool masked = key0 + kStep - 1 > plo ||
+                        (a.window > 0 && key0 <= phi - a.window && key0 + kStep - 1 >= a.sinks) || !alive[sr][0] || !alive[sr][1];
+          if (masked)
+            step_max<true>(a, ts, ksc[sr], alive[sr], pos, key0, mx);
+          else
+            step_max<false>(a, ts, ksc[sr], alive[sr], pos, key0, mx);
+          bool grow = false;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k0 = key0 + kv::kBlock * h, k1 = k0 + kv::kBlock - 1;
-            masked[h] = !alive[sr][h] || k1 > plo || (a.window > 0 && k0 <= phi - a.window && k1 >= a.sinks);
+          for (int r = 0; r < 4; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            grow = grow || mx[r] > m[r] + kSlack;
           }
-          // pass one: the row's maximum
-          float mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(ts + 32 * c, v);
-            wait_ld();
-            float z[32];
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(&ksc[sr][32 * c + x]);
-              unpack2(mul2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), pack2(k4.x, k4.y)), z[x], z[x + 1]);
-              unpack2(mul2(pack2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), pack2(k4.z, k4.w)), z[x + 2],
-                      z[x + 3]);
-            }
-            if (masked[c >> 1]) {
-              const int kb = key0 + 32 * c;
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!alive[sr][c >> 1] || !sees(a, pos, kb + x)) z[x] = -INFINITY;
-            }
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) mx = fmaxf(mx, fmaxf(z[x], z[x + 1]));
-          }
-          const bool grow = mx > m + kSlack || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? mx : m, f = grow ? exp2_approx(m - mn) : 1.f;
-            m = mn;
-            l *= f;
+            float f[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const bool up = mx[r] > m[r] + kSlack;
+              f[r] = up ? exp2_approx(m[r] - mx[r]) : 1.f;
+              m[r] = up ? mx[r] : m[r];
+              l[r] *= f[r];
+            }
             if (j > 0) {  // S of this step follows P V of the step before: O is at rest
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld32(to + 32 * c, v);
-                wait_ld();
 #pragma unroll
-                for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
-                tmem_st32(to + 32 * c, v);
+                for (int e = 0; e < 2; ++e) {
+                  uint32_t v[16];
+                  tmem_ld_frag32(to + e * half + 32 * c, v);
+                  wait_ld();
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f[2 * e + ((x >> 1) & 1)]);
+                  tmem_st_frag32(to + e * half + 32 * c, v);
+                }
               }
               wait_st();
             }
           }
-          const float mu = m == -INFINITY ? 0.f : m;
-          const f2 mneg = pack2(-mu, -mu);
-          // pass two: P over S, 64 keys at a time
+          uint64_t mneg[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pr[32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t v[32];
-              tmem_ld32(ts + 64 * h + 32 * c, v);
-              wait_ld();
-              const int kb = 64 * h + 32 * c;
-              f2 sum = pack2(0.f, 0.f);
-#pragma unroll
-              for (int x = 0; x < 32; x += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(&ksc[sr][kb + x]);
-                const float4 v4 = *reinterpret_cast<const float4*>(&vsc[sr][kb + x]);
-                float e[4];
-                unpack2(fma2(pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), pack2(k4.x, k4.y), mneg), e[0], e[1]);
-                unpack2(fma2(pack2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), pack2(k4.z, k4.w), mneg), e[2],
-                        e[3]);
-                bool see[4];
-                if (masked[h]) {
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) {
-                    see[y] = alive[sr][h] && sees(a, pos, key0 + kb + x + y);
-                    if (!see[y]) e[y] = -INFINITY;
-                  }
-                }
-#pragma unroll
-                for (int y = 0; y < 4; ++y) e[y] = exp2_approx(e[y]);
-                const f2 e01 = pack2(e[0], e[1]), e23 = pack2(e[2], e[3]);
-                sum = add2(sum, add2(e01, e23));
-                float q[4];
-                unpack2(mul2(e01, pack2(v4.x, v4.y)), q[0], q[1]);
-                unpack2(mul2(e23, pack2(v4.z, v4.w)), q[2], q[3]);
-                if (masked[h]) {  // a key that is not seen has weight 0 whatever its value's scale is
-#pragma unroll
-                  for (int y = 0; y < 4; ++y)
-                    if (!see[y]) q[y] = 0.f;
-                }
-                pr[16 * c + x / 2] = bf16x2(q[0], q[1]);
-                pr[16 * c + x / 2 + 1] = bf16x2(q[2], q[3]);
-              }
-              float s0, s1;
-              unpack2(sum, s0, s1);
-              l += s0 + s1;
-            }
-            tmem_st32(ts + 32 * h, pr);
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[t][h]);
-          }
+          for (int r = 0; r < 4; ++r) mneg[r] = twice(m[r] == -INFINITY ? 0.f : -m[r]);
+          if (masked)
+            step_probs<true>(a, ts, ksc[sr], vsc[sr], alive[sr], pos, key0, mneg, l, p_full[t]);
+          else
+            step_probs<false>(a, ts, ksc[sr], vsc[sr], alive[sr], pos, key0, mneg, l, p_full[t]);
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_full[t], (uint32_t)(pieces & 1)));
+        ok = ok && __all_sync(0xffffffffu, ring_wait(&o_full[t], (uint32_t)(pieces & 1)));
         ++pieces;
         // ---- epilogue: the outputs, or a partial
         if (ok) {
           fence_after();
-          const bool mine = kTile * t + row < w.t.nrows;
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          uint16_t* const op = a.out + (int64_t)(w.g.s.row0 + rr / a.group) * a.out_stride +
-                               (w.head * a.group + rr % a.group) * D;
+          float inv[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float x = l[r];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            inv[r] = whole ? (x == 0.f ? 0.f : 1.f / x) : x;  // a partial keeps the sum
+          }
           float* const part = a.partial + (size_t)(2 * blockIdx.x + (u != u0)) * C::kPiece;
+          uint16_t* op[4];
 #pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int rr = w.t.r0 + wr + 8 * r;
+            op[r] = a.out + (int64_t)(w.g.s.row0 + rr / a.group) * a.out_stride + (w.head * a.group + rr % a.group) * D +
+                    2 * ft;
+          }
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tmem_ld32(to + 32 * c, v);
+            uint32_t v[2][16];
+            tmem_ld_frag32(to + 32 * c, v[0]);
+            tmem_ld_frag32(to + half + 32 * c, v[1]);
             wait_ld();
-            if (mine && whole) {
 #pragma unroll
-              for (int x = 0; x < 32; x += 8) {
-                uint32_t o[4];
+            for (int r = 0; r < 4; ++r) {
+              if (wr + 8 * r >= w.t.nrows) continue;
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  o[y] = bf16x2(__uint_as_float(v[x + 2 * y]) * inv, __uint_as_float(v[x + 2 * y + 1]) * inv);
-                *reinterpret_cast<uint4*>(op + 32 * c + x) = make_uint4(o[0], o[1], o[2], o[3]);
+              for (int x = 0; x < 4; ++x) {
+                const float o0 = __uint_as_float(v[r >> 1][4 * x + 2 * (r & 1)]);
+                const float o1 = __uint_as_float(v[r >> 1][4 * x + 2 * (r & 1) + 1]);
+                if (whole)
+                  *reinterpret_cast<uint32_t*>(op[r] + 32 * c + 8 * x) = bf16x2(o0 * inv[r], o1 * inv[r]);
+                else
+                  *reinterpret_cast<float2*>(part + (wr + 8 * r) * D + 32 * c + 8 * x + 2 * ft) = make_float2(o0, o1);
               }
-            } else if (mine) {
-#pragma unroll
-              for (int x = 0; x < 32; x += 4)
-                *reinterpret_cast<uint4*>(part + ((size_t)(8 * c + x / 4) * kRows + kTile * t + row) * 4) =
-                    make_uint4(v[x], v[x + 1], v[x + 2], v[x + 3]);
             }
           }
-          if (mine && !whole)
-            *reinterpret_cast<float2*>(part + kRows * D + 2 * (kTile * t + row)) = make_float2(m, l);
+          if (!whole && ft == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (wr + 8 * r < w.t.nrows)
+                *reinterpret_cast<float2*>(part + kRows * D + 2 * (wr + 8 * r)) = make_float2(m[r], inv[r]);
+          }
           fence_before();
         }
       }
@@ -742,40 +896,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int c0 = (int)(((w.ia + 1) * G - 1) / U), c1 = (int)(((w.ia + w.t.n) * G - 1) / U);
         if (threadIdx.x == 0) s_last = atom_add_acq_rel(a.tickets + c0, 1u) == (uint32_t)(c1 - c0);
         asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (s_last) merge_rows<D>(a, w, c0, c1, G, U);
         if (s_last) {
-          const int pad = (w.t.nrows + 31) / 32 * 32;
-          for (int x = threadIdx.x; x < pad * (D / 4); x += 32 * kSoftWarps) {
-            const int r = x % pad, d4 = x / pad;
-            if (r >= w.t.nrows) continue;
-            float mm = -INFINITY, ll = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              // the tile's piece is its CTA's first unless the tile begins inside that CTA's range
-              const float* pp = a.partial + (size_t)(2 * c + (U * c / G < w.ia)) * C::kPiece;
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(pp + kRows * D + 2 * r));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + ((size_t)d4 * kRows + r) * 4));
-              const float mn = fmaxf(mm, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-              const float f0 = exp2_approx(mm - mu), f1 = exp2_approx(ml.x - mu);
-              mm = mn;
-              ll = fmaf(f1, ml.y, f0 * ll);
-              o.x = fmaf(f1, v.x, f0 * o.x);
-              o.y = fmaf(f1, v.y, f0 * o.y);
-              o.z = fmaf(f1, v.z, f0 * o.z);
-              o.w = fmaf(f1, v.w, f0 * o.w);
-            }
-            const int rr = w.t.r0 + r;
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            uint16_t* const op = a.out + (int64_t)(w.g.s.row0 + rr / a.group) * a.out_stride +
-                                 (w.head * a.group + rr % a.group) * D + 4 * d4;
-            *reinterpret_cast<uint2*>(op) = make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
-          }
           if (threadIdx.x == 0) a.tickets[c0] = 0u;
         }
       }
       step += n;
       u = ue;
-      if (u < u1) w.next(a, pre);
+      if (u < u1) advance();
     }
     if (!ok && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
   }
