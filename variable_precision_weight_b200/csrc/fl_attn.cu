@@ -198,12 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   __shared__ long long pre[FL_KV_MAX_SEQS + 1];
   __shared__ long long wsum[kWarps];
   __shared__ float sm_m[kWarps][R], sm_l[kWarps][R];
-  __shared__ int s_last;
+  __shared__ int s_last, s_items;
   float* const join = reinterpret_cast<float*>(smem + NS * C::kRec);
 
   pdl_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    s_items = 0;
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
@@ -215,14 +216,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   // ---- units before each sequence
   const int n_seqs = a.b.n_seqs, per = (n_seqs + kConsumers - 1) / kConsumers;
   long long mine = 0, inc = 0;
+  __syncthreads();
   if (warp < kWarps) {
     bool bad = false;
+    int items = 0;
     for (int k = 0; k < per; ++k) {
       const int i = threadIdx.x * per + k;
       if (i >= n_seqs) break;
       const Geo g = geo_of(a, i, &bad);
       mine += (long long)a.kv_heads * ((g.s.n * a.group + R - 1) / R) * g.np;
+      if (g.np > 0) items = min(items + a.kv_heads * ((g.s.n * a.group + R - 1) / R), 1 << 20);
     }
+    items = __reduce_add_sync(0xffffffffu, min(items, 1 << 20));
+    if (lane == 0 && items > 0) atomicAdd(&s_items, items);
     if (bad && blockIdx.x == 0) atomicMax(&g_error, (int)kv::kErrSeq);
     inc = mine;
 #pragma unroll
@@ -252,8 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   }
   __syncthreads();
   const long long U = pre[n_seqs];
-  // a CTA takes at least one unit per warp, so that short calls join in shared memory only
-  const int G = (int)min((long long)gridDim.x, (U + kWarps - 1) / kWarps);
+  // A CTA takes at least one unit per warp; where two per warp and item would do, one CTA per item,
+  // so that items of equal lengths are not cut (a join through the workspace costs more than the
+  // second unit: one stream of 517 tokens took 14.0 us cut, 13.0 us so).
+  const long long items = s_items;
+  const int G = items <= gridDim.x && U <= 2 * kWarps * items ? (int)items
+                                                              : (int)min((long long)gridDim.x, (U + kWarps - 1) / kWarps);
   if ((int)blockIdx.x >= G) return;
   const long long u0 = U * blockIdx.x / G, u1 = U * (blockIdx.x + 1) / G;
 
@@ -587,10 +597,15 @@ extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* 
   a.tickets = reinterpret_cast<uint32_t*>(wsb + wl.tickets);
   a.partial = reinterpret_cast<float*>(wsb + wl.partial);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  fl_status s = D == 64 ? (nt == 1 ? attn::launch<64, 1>(a, nsm, st) : attn::launch<64, 2>(a, nsm, st))
-                        : (nt == 1 ? attn::launch<128, 1>(a, nsm, st) : attn::launch<128, 2>(a, nsm, st));
-  if (s || max_rows <= attn::kSmallRows) return s;
-  a.min_rows = attn::kSmallRows + 1;
+  // One sequence that may be a chunk: the chunk kernel takes it whatever its length turns out to be,
+  // and a prompt saves the other launch (about 5 us).
+  const bool both = max_rows > attn::kSmallRows && batch->n_seqs > 1;
+  if (both || max_rows <= attn::kSmallRows) {
+    const fl_status s = D == 64 ? (nt == 1 ? attn::launch<64, 1>(a, nsm, st) : attn::launch<64, 2>(a, nsm, st))
+                                : (nt == 1 ? attn::launch<128, 1>(a, nsm, st) : attn::launch<128, 2>(a, nsm, st));
+    if (s || !both) return s;
+  }
+  a.min_rows = both ? attn::kSmallRows + 1 : 1;
   a.max_rows = 0x7fffffff;
   a.tickets = reinterpret_cast<uint32_t*>(wsb + wl.tc_tickets);
   a.partial = reinterpret_cast<float*>(wsb + wl.tc_partial);

@@ -355,13 +355,14 @@ __device__ __forceinline__ void step_probs(const Args& a, uint32_t ts, const flo
   }
 }
 
-// Joins the pieces of a tile that CTAs c0 .. c1 left, in that order: a warp per row, four rows at a
+// Joins the pieces of a tile that CTAs c0 .. c1 left, in that order: a warp per row, eight rows at a
 // time so that enough loads are in flight.
 template <int D>
 __device__ __forceinline__ void merge_rows(const Args& a, const Walk& w, int c0, int c1, int G, long long U) {
   using C = Cfg<D>;
-  constexpr int kE = D / 32, kB = 4;  // elements of a lane, rows at a time
+  constexpr int kE = D / 32, kB = 8;  // elements of a lane, rows at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool inside = U * c0 / G < w.ia;
   for (int r0 = warp; r0 < w.t.nrows; r0 += kB * kSoftWarps) {
     float m[kB], l[kB], o[kB][kE];
 #pragma unroll
@@ -374,7 +375,7 @@ __device__ __forceinline__ void merge_rows(const Args& a, const Walk& w, int c0,
 #pragma unroll 2
     for (int c = c0; c <= c1; ++c) {
       // the tile's piece is its CTA's first unless the tile begins inside that CTA's range
-      const float* pp = a.partial + (size_t)(2 * c + (U * c / G < w.ia)) * C::kPiece;
+      const float* pp = a.partial + (size_t)(2 * c + (c == c0 && inside)) * C::kPiece;
       float v[kB][kE];
       float2 ml[kB];
 #pragma unroll
