@@ -221,6 +221,67 @@ def test_attend_prompt_chunks(env, kvh, group, D, lens, news, levels):
     c.untouched(got)
 
 
+@pytest.mark.parametrize("kvh,group,D", [(1, 1, 64), (2, 2, 128), (1, 8, 64), (1, 32, 128)])
+@pytest.mark.parametrize("rows", [31, 32, 33, 127, 128, 129, 255, 256, 257, 513])
+def test_attend_row_counts(env, kvh, group, D, rows):
+    """Query rows per key/value head around the kernels' limits and the tiles' sizes, alone and among others."""
+    torch, fl = env
+    heads, new = kvh * group, max(1, rows // group)
+    for lens, news in (([new + 700], [new]), ([new, 90, new + 130], [new, 1, max(1, new - 1)])):
+        c = Case(torch, fl, lens, news, kvh, D, seed=rows + group, rows=sum(news) + 2, levels=(2, 4, 4, 0))
+        q = c.q(heads)
+        got = c.attend(q, heads, D ** -0.5)
+        fl.fl_device_status()
+        c.check(got, q, heads, D ** -0.5)
+        c.untouched(got)
+
+
+@pytest.mark.parametrize("kvh,group,D,n,new", [(1, 1, 64, 9000, 40), (2, 2, 128, 6000, 130), (1, 4, 64, 5000, 65)])
+def test_attend_chunk_cut_into_many_pieces(env, kvh, group, D, n, new):
+    """One tile of rows whose keys are spread over most of the GPU, and joined."""
+    torch, fl = env
+    heads = kvh * group
+    c = Case(torch, fl, [n], [new], kvh, D, seed=n, levels=(2, 4))
+    q = c.q(heads, 2.0)
+    for window, sinks in ((0, 0), (3000, 70)):
+        got = c.attend(q, heads, 0.1, window, sinks)
+        fl.fl_device_status()
+        c.check(got, q, heads, 0.1, window, sinks)
+        assert np.array_equal(c.attend(q, heads, 0.1, window, sinks), got)
+
+
+def test_chunk_sized_call_with_fewer_tokens(env):
+    """max_new sizes the launch only: one token, or none, in calls sized for a chunk."""
+    torch, fl = env
+    for lens, news in (([300], [1]), ([1], [1]), ([0], [0]), ([300, 77], [1, 5]), ([300, 77], [0, 0])):
+        c = Case(torch, fl, lens, news, 2, 64, seed=3, rows=300, max_new=300)
+        q = c.q(4)
+        got = c.attend(q, 4, 0.1)
+        fl.fl_device_status()
+        c.check(got, q, 4, 0.1)
+        c.untouched(got)
+
+
+def test_two_streams_with_their_own_workspaces(env):
+    torch, fl = env
+    cs = [Case(torch, fl, [2500, 800], [300, 1], 2, 128, seed=21), Case(torch, fl, [3000], [2], 2, 128, seed=22)]
+    qs = [c.q(4) for c in cs]
+    want = [c.attend(q, 4, 0.1) for c, q in zip(cs, qs)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    spaces = [c.workspace(4) for c in cs]
+    d_q = [dev(torch, q) for q in qs]
+    outs = [[torch.zeros((c.rows, 4, 128), dtype=torch.int16, device="cuda") for _ in range(4)] for c in cs]
+    torch.cuda.synchronize()
+    for r in range(4):
+        for c, q, s, (ws, n), o in zip(cs, d_q, streams, spaces, outs):
+            fl.fl_attn_paged(c.cache, c.batch, None, q, 512, 4, 0.1, 0, 0, o[r], 512, ws, n, s)
+    torch.cuda.synchronize()
+    fl.fl_device_status()
+    for w, o in zip(want, outs):
+        for x in o:
+            assert np.array_equal(x.cpu().numpy().view(np.uint16), w)
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (63, 0), (64, 4), (65, 64), (200, 65), (100, 5000), (5000, 4),
                                           (2 ** 31 - 1, 2 ** 31 - 1)])
 @pytest.mark.parametrize("new", [1, 7, 150])

@@ -98,17 +98,6 @@ __device__ __forceinline__ void unpack_word(uint32_t hi, uint32_t lo, uint32_t (
   }
 }
 
-// Wait on an mbarrier phase: polls that sleep up to a microsecond each, a bounded number of them
-// (about a second). Short on purpose: these kernels wait in many places, and their loops have to
-// stay in the instruction cache.
-__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
-#pragma unroll 1
-  for (int i = 0; i < (1 << 20); ++i)
-    if (mbar_try_sleep(a, parity, 1000)) return true;
-  return false;
-}
-
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ float lds32(const uint8_t* p) { return *reinterpret_cast<const float*>(p); }
 

@@ -44,6 +44,7 @@ constexpr int kTile = 128, kRows = 2 * kTile;  // rows of an MMA, of a unit
 constexpr int kStep = 2 * kv::kBlock;          // keys of a unit
 constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 8, kMmaWarp = 16, kLoadWarp = 17;
 constexpr int kScaleRing = 4;  // steps whose scales are held; the operand ring keeps fewer in flight
+constexpr int kCutSteps = 5;   // what cutting a tile costs, in steps
 constexpr float kSlack = 8.f;  // a row's maximum moves when it grows by more than this (log2)
 
 template <int D>
@@ -184,14 +185,14 @@ struct Walk {
     g = geo_of(a, i, &bad);
     tiles = tiles_of(a, g);
   }
-  __device__ void seek(const Args& a, const long long* pre, long long u) {
+  __device__ void seek(const Args& a, const long long* pre, long long u, bool by_tile) {
     const int lane = threadIdx.x & 31;
     at_seq(a, find_seq(pre, a.b.n_seqs, u));
     const long long per = (pre[i + 1] - pre[i]) / a.kv_heads;
     head = (int)((u - pre[i]) / per);
     ia = pre[i] + head * per;
     for (tau = 0;; tau += 32) {
-      const int mine = tau + lane < tiles ? tile_of(a, g, tau + lane).n : 0;
+      const int mine = tau + lane >= tiles ? 0 : by_tile ? 1 : tile_of(a, g, tau + lane).n;
       long long inc = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   __shared__ int alive[kScaleRing][2];
   __shared__ long long pre[FL_KV_MAX_SEQS + 1];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_last;
+  __shared__ int s_last, s_tiles, s_longest;
   __shared__ Walk walks[kLoadWarp + 1];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* const q_smem = smem;
@@ -438,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   pdl_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    s_tiles = s_longest = 0;
     for (int s = 0; s < NR; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], kConvWarps);
@@ -457,46 +459,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     fence_mbar_init();
   }
   pdl_wait();
+  __syncthreads();
 
-  // ---- units before each sequence: a warp per sequence, a lane per tile
+  // ---- units before each sequence: a warp per sequence, a lane per tile. Where no tile is longer
+  // than an even share and what a cut costs (about five steps: two more ends of a tile and a join),
+  // the unit is a whole tile: a 1021-token prompt's 128 tiles of 1 to 8 steps, 3.9 a share.
   const int n_seqs = a.b.n_seqs;
-  {
+  auto scan = [&](bool tiles_only) {
     bool bad = false;
+    int longest = 0;
     for (int i = warp; i < n_seqs; i += kThreads / 32) {
       const Geo g = geo_of(a, i, &bad);
       const int tiles = tiles_of(a, g);
-      long long sum = 0;
-      for (int tau = lane; tau < tiles; tau += 32) sum += tile_of(a, g, tau).n;
+      long long sum = tiles;
+      if (!tiles_only) {
+        sum = 0;
+        for (int tau = lane; tau < tiles; tau += 32) {
+          const int n = tile_of(a, g, tau).n;
+          sum += n;
+          longest = max(longest, n);
+        }
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) atomicAdd(&s_tiles, min(tiles, 1024) * a.kv_heads);
+      }
       if (lane == 0) pre[i] = sum * a.kv_heads;
     }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) atomicMax(&s_longest, longest);
     if (bad && blockIdx.x == 0) atomicMax(&g_error, (int)kv::kErrSeq);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    const int per = (n_seqs + 31) / 32, i0 = min(lane * per, n_seqs), i1 = min(i0 + per, n_seqs);
-    long long sum = 0;
-    for (int i = i0; i < i1; ++i) sum += pre[i];
-    long long inc = sum;
+    __syncthreads();
+    if (warp == 0) {
+      const int per = (n_seqs + 31) / 32, i0 = min(lane * per, n_seqs), i1 = min(i0 + per, n_seqs);
+      long long sum = 0;
+      for (int i = i0; i < i1; ++i) sum += pre[i];
+      long long inc = sum;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += o;
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      long long before = inc - sum;
+      for (int i = i0; i < i1; ++i) {
+        const long long x = pre[i];
+        pre[i] = before;
+        before += x;
+      }
+      if (lane == 31) pre[n_seqs] = inc;
     }
-    long long before = inc - sum;
-    for (int i = i0; i < i1; ++i) {
-      const long long x = pre[i];
-      pre[i] = before;
-      before += x;
-    }
-    if (lane == 31) pre[n_seqs] = inc;
-  }
-  __syncthreads();
+    __syncthreads();
+  };
+  scan(false);
   const long long U = pre[n_seqs];
-  const int G = (int)min((long long)gridDim.x, U);
+  const int share = (int)min(U / gridDim.x, (long long)1 << 30);
+  const bool by_tile = (unsigned)s_tiles <= gridDim.x && s_longest <= share + kCutSteps;
+  const int G = by_tile ? s_tiles : (int)min((long long)gridDim.x, U);
   if ((int)blockIdx.x >= G) return;
-  const long long u0 = U * blockIdx.x / G, u1 = U * (blockIdx.x + 1) / G;
+  if (by_tile) {
+    __syncthreads();
+    scan(true);
+  }
+  long long u0 = by_tile ? blockIdx.x : U * blockIdx.x / G, u1 = U * (blockIdx.x + 1) / G;
 
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u)
@@ -512,7 +535,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   Walk& w = walks[min(warp, kLoadWarp)];
   if (warp <= kLoadWarp) {
     Walk x;
-    x.seek(a, pre, u0);
+    x.seek(a, pre, u0, by_tile);
+    if (by_tile) {  // the CTA's units are the tile's steps
+      x.ia = u0 = 0;
+      u1 = x.t.n;
+    }
     if (lane == 0) w = x;
     __syncwarp();
   }
@@ -534,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     auto emit = [&](const uint8_t* src, int lv, bool values) {
       const int s = unit % NR;
       if (failed) return;
-      if (unit >= NR && !__all_sync(0xffffffffu, ring_wait(&raw_empty[s], (uint32_t)((unit / NR - 1) & 1)))) {
+      if (unit >= NR && !__all_sync(0xffffffffu, mbar_wait(&raw_empty[s], (uint32_t)((unit / NR - 1) & 1)))) {
         failed = true;
         return;
       }
@@ -603,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (failed && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
     // no copy may still be landing when the CTA exits
     for (int k = max(0, unit - NR); k < unit; ++k)
-      if (!ring_wait(&raw_full[k % NR], (uint32_t)((k / NR) & 1)) && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+      if (!mbar_wait(&raw_full[k % NR], (uint32_t)((k / NR) & 1)) && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA issue: one thread
     if (elect_one()) {
@@ -611,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       bool ok = true;
       int base = 0;               // operands before the piece
       uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-      auto op_wait = [&](int o) { ok = ok && ring_wait(&op_full[o % NS], (uint32_t)((o / NS) & 1)); };
+      auto op_wait = [&](int o) { ok = ok && mbar_wait(&op_full[o % NS], (uint32_t)((o / NS) & 1)); };
       auto scores = [&](int t, int o) {
         const uint64_t qd = q_desc + (uint64_t)(t * (kTile * D * 2 / 16)), kd = op_desc + (uint64_t)((o % NS) * (C::kSlotBytes / 16));
 #pragma unroll
@@ -626,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int n = (int)(ue - u), nt = w.t.nrows > kTile ? 2 : 1;
         op_wait(base);
         for (int t = 0; t < nt && ok; ++t) {
-          ok = ring_wait(&q_full[t], nq[t]++ & 1u);
+          ok = mbar_wait(&q_full[t], nq[t]++ & 1u);
           fence_after();
           if (ok) scores(t, base);
         }
@@ -639,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const uint64_t vd = op_desc + (uint64_t)((vo % NS) * (C::kSlotBytes / 16));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              ok = ok && ring_wait(&p_full[t][h], np[t] & 1u);
+              ok = ok && mbar_wait(&p_full[t][h], np[t] & 1u);
               if (!ok) break;
               fence_after();
 #pragma unroll
@@ -662,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (u < u1) w.next(a, pre);
       }
       // every MMA is complete before TMEM is freed: the last commit tracks all of them
-      if (ok && base > 0) ok = ring_wait(&op_empty[(base - 1) % NS], (uint32_t)(((base - 1) / NS) & 1));
+      if (ok && base > 0) ok = mbar_wait(&op_empty[(base - 1) % NS], (uint32_t)(((base - 1) / NS) & 1));
       if (!ok) atomicMax(&g_error, (int)kv::kErrWait);
     }
     __syncwarp();
@@ -682,12 +709,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (int o = 0; o < 2 * n && !failed; ++o, ++op) {
           const bool values = o == 2 * n - 1 || (o > 0 && o % 2 == 0);
           const int os = op % NS, sr = step % kScaleRing;
-          failed = op >= NS && !__all_sync(0xffffffffu, ring_wait(&op_empty[os], (uint32_t)((op / NS - 1) & 1)));
+          failed = op >= NS && !__all_sync(0xffffffffu, mbar_wait(&op_empty[os], (uint32_t)((op / NS - 1) & 1)));
           uint8_t* const dst = op_smem + os * C::kSlotBytes;
 #pragma unroll 1
           for (int pg = 0; pg < 2 && !failed; ++pg, ++unit) {
             const int s = unit % NR;
-            if (!__all_sync(0xffffffffu, ring_wait(&raw_full[s], (uint32_t)((unit / NR) & 1)))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[s], (uint32_t)((unit / NR) & 1)))) {
               failed = true;
               break;
             }
@@ -790,8 +817,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         float l[4] = {0.f, 0.f, 0.f, 0.f};
         for (int j = 0; j < n && ok; ++j, ++cnt) {
           const int sr = (step + j) % kScaleRing, key0 = kStep * step_at(w.t, p0 + j);
-          ok = __all_sync(0xffffffffu, ring_wait(&sc_full[sr], (uint32_t)(((step + j) / kScaleRing) & 1)) &&
-                                           ring_wait(&s_full[t], (uint32_t)(cnt & 1)));
+          ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[sr], (uint32_t)(((step + j) / kScaleRing) & 1)) &&
+                                           mbar_wait(&s_full[t], (uint32_t)(cnt & 1)));
           if (!ok) break;
           fence_after();
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -841,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           else
             step_probs<false>(a, ts, ksc[sr], vsc[sr], alive[sr], pos, key0, mneg, l, p_full[t]);
         }
-        ok = ok && __all_sync(0xffffffffu, ring_wait(&o_full[t], (uint32_t)(pieces & 1)));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_full[t], (uint32_t)(pieces & 1)));
         ++pieces;
         // ---- epilogue: the outputs, or a partial
         if (ok) {
