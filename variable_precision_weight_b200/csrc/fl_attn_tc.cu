@@ -19,8 +19,8 @@
 // rows, step of 128 keys = two pages); rows are (token, head of the group) pairs. Each tile's
 // units are the steps that some row of it sees. All units of the call, in order, are cut into
 // equal contiguous ranges, one per CTA.
-//  * Warp 17 streams the pages' planes into a ring (bulk copies), keys of a step with its scales,
-//    then the values of the step before.
+//  * Warp 17 streams the pages' planes into a ring (bulk copies): a step's keys with all scales, its
+//    values.
 //  * Warps 8-15 turn nibbles into bf16 and write them, 128-byte swizzled, as the K-major B
 //    operands of both products (K as [key][dim], V as [dim][key]: the cache's fragment order gives
 //    eight consecutive elements of either per 16-byte store).
@@ -586,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const long long ue = min(u1, w.ia + w.t.n);
       const int p0 = (int)(u - w.ia), p1 = (int)(ue - w.ia);
       const int blocks = w.g.s.len / kv::kBlock + (w.g.s.len % kv::kBlock != 0);
-      const uint8_t *src = nullptr, *prev_src[2] = {nullptr, nullptr};
-      int lv = 0, prev_lv[2] = {0, 0};
-      for (int p = p0; p <= p1 && !failed; ++p) {  // keys of step p, values of the step before
+      const uint8_t* src = nullptr;
+      int lv = 0;
+      for (int p = p0; p < p1 && !failed; ++p) {
         const int k = (p - p0) & 15;
         if (k == 0) {  // sixteen steps' table entries at once, two lanes per step
           lv = 0;
@@ -617,14 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           cur_lv[e] = __shfl_sync(0xffffffffu, lv, 2 * k + e);
         }
 #pragma unroll 1
-        for (int e = p < p1 ? 0 : 2; e < (p > p0 ? 4 : 2); ++e)
-          emit(e == 0 ? cur_src[0] : e == 1 ? cur_src[1] : e == 2 ? prev_src[0] : prev_src[1],
-               e == 0 ? cur_lv[0] : e == 1 ? cur_lv[1] : e == 2 ? prev_lv[0] : prev_lv[1], e >= 2);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          prev_src[e] = cur_src[e];
-          prev_lv[e] = cur_lv[e];
-        }
+        for (int e = 0; e < 4; ++e)  // the step's keys, then its values
+          emit(e & 1 ? cur_src[1] : cur_src[0], e & 1 ? cur_lv[1] : cur_lv[0], e >= 2);
       }
       u = ue;
       if (u < u1) advance();
@@ -661,9 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         if (ok) mma_commit(&op_empty[base % NS]);
         for (int j = 0; j < n && ok; ++j) {
-          const int vo = base + (j == n - 1 ? 2 * n - 1 : 2 * j + 2), ko = base + 2 * j + 1;
+          const int vo = base + 2 * j + 1, ko = vo + 1;
           op_wait(vo);
-          if (j + 1 < n) op_wait(ko);
           for (int t = 0; t < nt && ok; ++t) {
             const uint64_t vd = op_desc + (uint64_t)((vo % NS) * (C::kSlotBytes / 16));
 #pragma unroll
@@ -681,6 +674,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (t == nt - 1) mma_commit(&op_empty[vo % NS]);
             if (j == n - 1) mma_commit(&o_full[t]);
             if (j + 1 < n) {
+              if (t == 0) {
+                op_wait(ko);
+                if (!ok) break;
+                fence_after();
+              }
               scores(t, ko);
               if (t == nt - 1) mma_commit(&op_empty[ko % NS]);
             }
@@ -699,7 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   } else if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------------------------------------------------------- raw ring -> operands
-    // in the order K0, K1, V0, K2, V1, .., V(n - 1) of each piece
+    // in the order K0, V0, K1, V1, .. : with three slots a step's keys then wait for the slot of the
+    // values two before, free before the scores of the step between are (keys first, K0, K1, V0, ..,
+    // took 761 us instead of 751 for 2048 tokens over 32k)
     {
       const int cw = warp - kConvWarp, g = lane >> 2, t = lane & 3;
       int unit = 0, op = 0, step = 0;
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int n = (int)(ue - u);
 #pragma unroll 1
         for (int o = 0; o < 2 * n && !failed; ++o, ++op) {
-          const bool values = o == 2 * n - 1 || (o > 0 && o % 2 == 0);
+          const bool values = o & 1;
           const int os = op % NS, sr = step % kScaleRing;
           failed = op >= NS && !__all_sync(0xffffffffu, mbar_wait(&op_empty[os], (uint32_t)((op / NS - 1) & 1)));
           uint8_t* const dst = op_smem + os * C::kSlotBytes;
