@@ -29,7 +29,8 @@
 //  * Warps 0-3 and 4-7: softmax of rows 0-127 and 128-255. Pass one over S (tensor memory) finds
 //    the rows' maxima, pass two writes P over S; then the epilogue.
 //  * A tile cut by a range boundary leaves partials in the workspace, joined in CTA order by the
-//    CTA that arrives last. Short prompts are not cut: a CTA takes a whole tile (kCutSteps).
+//    CTA that arrives last. Where it costs little balance, every tile is cut into the same number
+//    of parts instead, one per CTA (one part: a whole tile).
 #include <algorithm>
 
 #include "fl_attn.cuh"
@@ -46,7 +47,7 @@ constexpr int kTile = 128, kRows = 2 * kTile;  // rows of an MMA, of a unit
 constexpr int kStep = 2 * kv::kBlock;          // keys of a unit
 constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 8, kMmaWarp = 16, kLoadWarp = 17;
 constexpr int kScaleRing = 4;  // steps whose scales are held; the operand ring keeps fewer in flight
-constexpr int kCutSteps = 5;   // what cutting a tile costs, in steps
+constexpr int kCutSteps = 8;   // what a range's second piece of a tile costs, in steps
 constexpr float kSlack = 8.f;  // a row's maximum moves when it grows by more than this (log2)
 
 template <int D>
@@ -177,6 +178,7 @@ __device__ __forceinline__ int step_at(const Tile& t, int p) { return p < t.sink
 // A warp's place in the list of units; every lane holds the same.
 struct Walk {
   int i, head, tau, tiles;
+  int cuts;      // parts of the tile, where every tile is cut alike
   long long ia;  // first unit of the tile
   Geo g;
   Tile t;
@@ -358,14 +360,27 @@ __device__ __forceinline__ void step_probs(const Args& a, uint32_t ts, const flo
   }
 }
 
-// Joins the pieces of a tile that CTAs c0 .. c1 left, in that order: a warp per row, eight rows at a
+// Word x of quad lane t and word t of quad lane x change places (all 32 lanes).
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int t) {
+  const bool odd = t & 1, upper = t & 2;
+  const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1);
+  const uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+  w[0] = odd ? x : w[0], w[1] = odd ? w[1] : x;
+  w[2] = odd ? y : w[2], w[3] = odd ? w[3] : y;
+  const uint32_t z0 = __shfl_xor_sync(0xffffffffu, upper ? w[0] : w[2], 2);
+  const uint32_t z1 = __shfl_xor_sync(0xffffffffu, upper ? w[1] : w[3], 2);
+  w[0] = upper ? z0 : w[0], w[2] = upper ? w[2] : z0;
+  w[1] = upper ? z1 : w[1], w[3] = upper ? w[3] : z1;
+}
+
+// Joins the pieces of a tile that CTAs c0 .. c1 left, in that order (inside: the tile begins inside
+// c0's range, so its piece is that CTA's second): a warp per row, eight rows at a
 // time so that enough loads are in flight.
 template <int D>
-__device__ __forceinline__ void merge_rows(const Args& a, const Walk& w, int c0, int c1, int G, long long U) {
+__device__ __forceinline__ void merge_rows(const Args& a, const Walk& w, int c0, int c1, bool inside) {
   using C = Cfg<D>;
   constexpr int kE = D / 32, kB = 8;  // elements of a lane, rows at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool inside = U * c0 / G < w.ia;
   for (int r0 = warp; r0 < w.t.nrows; r0 += kB * kSoftWarps) {
     float m[kB], l[kB], o[kB][kE];
 #pragma unroll
@@ -377,7 +392,6 @@ __device__ __forceinline__ void merge_rows(const Args& a, const Walk& w, int c0,
     }
 #pragma unroll 2
     for (int c = c0; c <= c1; ++c) {
-      // the tile's piece is its CTA's first unless the tile begins inside that CTA's range
       const float* pp = a.partial + (size_t)(2 * c + (c == c0 && inside)) * C::kPiece;
       float v[kB][kE];
       float2 ml[kB];
@@ -431,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   __shared__ int alive[kScaleRing][2];
   __shared__ long long pre[FL_KV_MAX_SEQS + 1];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_last, s_tiles, s_longest;
+  __shared__ int s_last, s_tiles, s_longest, s_parts;
   __shared__ Walk walks[kLoadWarp + 1];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* const q_smem = smem;
@@ -463,9 +477,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   pdl_wait();
   __syncthreads();
 
-  // ---- units before each sequence: a warp per sequence, a lane per tile. Where no tile is longer
-  // than an even share and what a cut costs (about five steps: two more ends of a tile and a join),
-  // the unit is a whole tile: a 1021-token prompt's 128 tiles of 1 to 8 steps, 3.9 a share.
+  // ---- units before each sequence: a warp per sequence, a lane per tile. Equal ranges of all units
+  // balance best but cut most tiles twice, and a range's two pieces each fill and drain the pipeline
+  // and pass through the workspace. So where tiles cut into equally many parts give no part much
+  // longer than a range (kCutSteps), CTAs take parts: a 1021-token prompt's 128 tiles of 1 to 8
+  // steps whole (60 -> 40 us), 64 tiles of 17 to 29 steps in two.
   const int n_seqs = a.b.n_seqs;
   auto scan = [&](bool tiles_only) {
     bool bad = false;
@@ -514,14 +530,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   scan(false);
   const long long U = pre[n_seqs];
   const int share = (int)min(U / gridDim.x, (long long)1 << 30);
-  const bool by_tile = (unsigned)s_tiles <= gridDim.x && s_longest <= share + kCutSteps;
-  const int G = by_tile ? s_tiles : (int)min((long long)gridDim.x, U);
+  const int parts = s_tiles > 0 ? (int)(gridDim.x / (unsigned)s_tiles) : 0;  // of a tile
+  const bool by_tile = parts > 0 && (s_longest + parts - 1) / parts <= share + kCutSteps;
+  const int G = by_tile ? s_tiles * parts : (int)min((long long)gridDim.x, U);
   if ((int)blockIdx.x >= G) return;
   if (by_tile) {
     __syncthreads();
     scan(true);
   }
-  long long u0 = by_tile ? blockIdx.x : U * blockIdx.x / G, u1 = U * (blockIdx.x + 1) / G;
+  if (threadIdx.x == 0) s_parts = by_tile ? parts : 0;  // (read at a join, after the next barrier)
+  long long u0 = by_tile ? blockIdx.x / parts : U * blockIdx.x / G, u1 = U * (blockIdx.x + 1) / G;
 
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u)
@@ -538,9 +556,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   if (warp <= kLoadWarp) {
     Walk x;
     x.seek(a, pre, u0, by_tile);
-    if (by_tile) {  // the CTA's units are the tile's steps
-      x.ia = u0 = 0;
-      u1 = x.t.n;
+    if (by_tile) {  // units are the tile's steps
+      const int cuts = min(parts, x.t.n), part = blockIdx.x % parts;  // a short tile has fewer
+      x.cuts = cuts;
+      x.ia = 0;
+      u0 = part < cuts ? (long long)x.t.n * part / cuts : 0;
+      u1 = part < cuts ? (long long)x.t.n * (part + 1) / cuts : 0;
     }
     if (lane == 0) w = x;
     __syncwarp();
@@ -889,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           for (int r = 0; r < 4; ++r) {
             const int rr = w.t.r0 + wr + 8 * r;
             op[r] = a.out + (int64_t)(w.g.s.row0 + rr / a.group) * a.out_stride + (w.head * a.group + rr % a.group) * D +
-                    2 * ft;
+                    8 * ft;
           }
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -899,15 +920,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             wait_ld();
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              if (wr + 8 * r >= w.t.nrows) continue;
+              // the four lanes of a row trade columns, so that each stores eight in a row
+              uint32_t e0[4], e1[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                const float o0 = __uint_as_float(v[r >> 1][4 * x + 2 * (r & 1)]);
-                const float o1 = __uint_as_float(v[r >> 1][4 * x + 2 * (r & 1) + 1]);
-                if (whole)
-                  *reinterpret_cast<uint32_t*>(op[r] + 32 * c + 8 * x) = bf16x2(o0 * inv[r], o1 * inv[r]);
-                else
-                  *reinterpret_cast<float2*>(part + (wr + 8 * r) * D + 32 * c + 8 * x + 2 * ft) = make_float2(o0, o1);
+                e0[x] = v[r >> 1][4 * x + 2 * (r & 1)];
+                e1[x] = v[r >> 1][4 * x + 2 * (r & 1) + 1];
+                if (whole) e0[x] = bf16x2(__uint_as_float(e0[x]) * inv[r], __uint_as_float(e1[x]) * inv[r]);
+              }
+              quad_transpose(e0, ft);
+              if (!whole) quad_transpose(e1, ft);
+              if (wr + 8 * r >= w.t.nrows) continue;
+              if (whole) {
+                *reinterpret_cast<uint4*>(op[r] + 32 * c) = make_uint4(e0[0], e0[1], e0[2], e0[3]);
+              } else {
+                uint4* const pp = reinterpret_cast<uint4*>(part + (wr + 8 * r) * D + 32 * c + 8 * ft);
+                pp[0] = make_uint4(e0[0], e1[0], e0[1], e1[1]);
+                pp[1] = make_uint4(e0[2], e1[2], e0[3], e1[3]);
               }
             }
           }
@@ -922,11 +951,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       if (!whole) {
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        // CTA of unit v: the largest c with U c / G <= v
-        const int c0 = (int)(((w.ia + 1) * G - 1) / U), c1 = (int)(((w.ia + w.t.n) * G - 1) / U);
+        int c0, c1;
+        bool inside = false;
+        if (s_parts > 0) {
+          c0 = blockIdx.x - blockIdx.x % s_parts;
+          c1 = c0 + w.cuts - 1;
+        } else {  // CTA of unit v: the largest c with U c / G <= v
+          const long long U = pre[n_seqs], G = min((long long)gridDim.x, U);
+          c0 = (int)(((w.ia + 1) * G - 1) / U);
+          c1 = (int)(((w.ia + w.t.n) * G - 1) / U);
+          inside = U * c0 / G < w.ia;
+        }
         if (threadIdx.x == 0) s_last = atom_add_acq_rel(a.tickets + c0, 1u) == (uint32_t)(c1 - c0);
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (s_last) merge_rows<D>(a, w, c0, c1, G, U);
+        if (s_last) merge_rows<D>(a, w, c0, c1, inside);
         if (s_last) {
           if (threadIdx.x == 0) a.tickets[c0] = 0u;
         }
