@@ -250,6 +250,22 @@ def test_attend_chunk_cut_into_many_pieces(env, kvh, group, D, n, new):
         assert np.array_equal(c.attend(q, heads, 0.1, window, sinks), got)
 
 
+@pytest.mark.parametrize("lens,news", [
+    ([6000, 300, 300, 300], [200, 290, 290, 290]),                  # one long tile per head among short ones
+    ([400 + 97 * i for i in range(20)], [40 + i for i in range(20)]),   # more tiles than the GPU has SMs
+    ([1500, 64, 700], [600, 64, 33])])
+def test_attend_chunks_in_equal_ranges(env, lens, news):
+    """Tiles of unequal lengths, cut anywhere by equal ranges of steps."""
+    torch, fl = env
+    c = Case(torch, fl, lens, news, 8, 64, seed=sum(news), rows=sum(news) + 4, levels=(2, 4))
+    q = c.q(8)
+    got = c.attend(q, 8, 0.125)
+    fl.fl_device_status()
+    c.check(got, q, 8, 0.125)
+    c.untouched(got)
+    assert np.array_equal(c.attend(q, 8, 0.125), got)
+
+
 def test_chunk_sized_call_with_fewer_tokens(env):
     """max_new sizes the launch only: one token, or none, in calls sized for a chunk."""
     torch, fl = env
