@@ -236,7 +236,8 @@ def test_attend_row_counts(env, kvh, group, D, rows):
         c.untouched(got)
 
 
-@pytest.mark.parametrize("kvh,group,D,n,new", [(1, 1, 64, 9000, 40), (2, 2, 128, 6000, 130), (1, 4, 64, 5000, 65)])
+@pytest.mark.parametrize("kvh,group,D,n,new", [(1, 1, 64, 9000, 40), (1, 1, 64, 9000, 200), (2, 2, 128, 6000, 130),
+                                                 (1, 4, 64, 5000, 65)])
 def test_attend_chunk_cut_into_many_pieces(env, kvh, group, D, n, new):
     """One tile of rows whose keys are spread over most of the GPU, and joined."""
     torch, fl = env
@@ -252,7 +253,7 @@ def test_attend_chunk_cut_into_many_pieces(env, kvh, group, D, n, new):
 
 @pytest.mark.parametrize("lens,news", [
     ([6000, 300, 300, 300], [200, 290, 290, 290]),                  # one long tile per head among short ones
-    ([400 + 97 * i for i in range(20)], [40 + i for i in range(20)]),   # more tiles than the GPU has SMs
+    ([400 + 97 * i for i in range(20)], [63 + i for i in range(20)]),   # more tiles than the GPU has SMs
     ([1500, 64, 700], [600, 64, 33])])
 def test_attend_chunks_in_equal_ranges(env, lens, news):
     """Tiles of unequal lengths, cut anywhere by equal ranges of steps."""

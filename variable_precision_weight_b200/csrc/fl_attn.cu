@@ -3,13 +3,13 @@
 // Mathematics: one pass over the keys with the running maximum m and sum l of the softmax in
 // powers of two; a row's state (m, l, o) of any set of keys joins another's by
 //   M = max(m1, m2), l = l1 2^(m1-M) + l2 2^(m2-M), o likewise,
-// so the keys are split freely. Codes enter the tensor-core products exactly as bf16 integers;
-// the key's scale multiplies its score column, the value's scale its probability.
+// so the keys are split freely. Codes enter the tensor-core products exactly (as bf16
+// values, fl_attn.cuh); the key's scale multiplies its score column, the value's its probability.
 //
 // Bound: HBM bytes of the visible records (512 + 128 D at D8, 512 + 64 D at D4 per page and head).
 // Measured: 8 streams of 45-49k tokens at D4, 112 us (63 us at the copy rate). The copies alone take
 // 88 us and the arithmetic alone 99: unpacking and the softmax, not the MMAs (16% of their pipe).
-// Eleven consumer warps instead of seven took 120 us.
+// Five, six or eleven consumer warps instead of seven took 127, 118 and 120 us.
 //
 // How: scores and outputs are computed transposed, S^T = K Q^T and O^T = V^T P^T, so that the 64
 // keys and the D dims fill the 16-row side of mma.m16n8k16 and the few query rows of one
@@ -500,20 +500,25 @@ struct Ws {
   size_t tickets, tc_tickets, partial, tc_partial, total;
 };
 
-// Sequences with more rows (new tokens x group) than this take the tcgen05 kernel.
-constexpr int kSmallRows = 32;
+// Sequences with more rows (new tokens x group) than this take the tcgen05 kernel, whose tile of 256
+// rows costs the same however few are used, while this one reads a page again for every 16 rows.
+// Measured over 3.5-4.5k tokens, this kernel against the other: 8 sequences of 8 heads, 64 rows 47
+// and 73 against 73 and 82 us (64, 128 dims), 96 rows 63 and 102 against 76 and 84, 128 rows 80 and
+// 130 against 76 and 86; one sequence, 96 rows 21 against 42, 128 rows 31 against 58 us: its few
+// tiles leave the other kernel mostly starts, ends and joins.
+static int small_rows(int n_seqs, int kv_heads) { return n_seqs * kv_heads <= 16 ? 128 : 64; }
 
 // Rows per tile by the largest number of rows a (sequence, head) has: eight columns cost half the
 // MMAs of sixteen.
 static int row_tiles(long long max_rows) { return max_rows <= 8 ? 1 : 2; }
 
-static Ws ws_layout(int nsm, int D, long long max_rows) {
+static Ws ws_layout(int nsm, int D, long long max_rows, int small) {
   Ws w;
   w.tickets = 0;
   w.tc_tickets = (size_t)kMaxGrid * 4;
   w.partial = 2 * (size_t)kMaxGrid * 4;
   w.tc_partial = w.partial + (size_t)nsm * 2 * (8 * row_tiles(max_rows)) * (D + 2) * 4;
-  w.total = w.tc_partial + (max_rows > kSmallRows ? attn_tc::partial_bytes(D, nsm) : 0);
+  w.total = w.tc_partial + (max_rows > small ? attn_tc::partial_bytes(D, nsm) : 0);
   return w;
 }
 
@@ -548,7 +553,7 @@ extern "C" size_t fl_attn_workspace_bytes(int n_seqs, int heads, int kv_heads, i
   using namespace fl;
   const int nsm = std::min(device_sm_count(), attn::kMaxGrid);
   if (nsm <= 0 || !attn::shape_ok(n_seqs, heads, kv_heads, head_dim, max_new)) return 0;
-  return attn::ws_layout(nsm, head_dim, (long long)max_new * (heads / kv_heads)).total;
+  return attn::ws_layout(nsm, head_dim, (long long)max_new * (heads / kv_heads), attn::small_rows(n_seqs, kv_heads)).total;
 }
 
 extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* batch, const uint8_t* levels,
@@ -574,7 +579,8 @@ extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* 
   if (units > 2147483647.0 || units * batch->n_seqs / nsm > 2147483647.0)
     return fail(FL_ERR_SHAPE, "%s: max_new=%d over max_blocks=%d is too large for one call", what, batch->max_new,
                 batch->max_blocks);
-  const attn::Ws wl = attn::ws_layout(nsm, D, max_rows);
+  const int small = attn::small_rows(batch->n_seqs, Hkv);
+  const attn::Ws wl = attn::ws_layout(nsm, D, max_rows, small);
   if (!workspace || workspace_bytes < wl.total)
     return fail(FL_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, workspace ? workspace_bytes : (size_t)0,
                 wl.total);
@@ -596,19 +602,19 @@ extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* 
   a.window = window;
   a.sinks = sinks;
   a.min_rows = 1;
-  a.max_rows = attn::kSmallRows;
+  a.max_rows = small;
   a.tickets = reinterpret_cast<uint32_t*>(wsb + wl.tickets);
   a.partial = reinterpret_cast<float*>(wsb + wl.partial);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // One sequence that may be a chunk: the chunk kernel takes it whatever its length turns out to be,
   // and a prompt saves the other launch (about 5 us).
-  const bool both = max_rows > attn::kSmallRows && batch->n_seqs > 1;
-  if (both || max_rows <= attn::kSmallRows) {
+  const bool both = max_rows > small && batch->n_seqs > 1;
+  if (both || max_rows <= small) {
     const fl_status s = D == 64 ? (nt == 1 ? attn::launch<64, 1>(a, nsm, st) : attn::launch<64, 2>(a, nsm, st))
                                 : (nt == 1 ? attn::launch<128, 1>(a, nsm, st) : attn::launch<128, 2>(a, nsm, st));
     if (s || !both) return s;
   }
-  a.min_rows = both ? attn::kSmallRows + 1 : 1;
+  a.min_rows = both ? small + 1 : 1;
   a.max_rows = 0x7fffffff;
   a.tickets = reinterpret_cast<uint32_t*>(wsb + wl.tc_tickets);
   a.partial = reinterpret_cast<float*>(wsb + wl.tc_partial);

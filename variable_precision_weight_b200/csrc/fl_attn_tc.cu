@@ -11,7 +11,7 @@
 //
 // Bound: per step of 128 keys and 256 query rows at D = 128 an SM needs 2048 cycles of MMA and
 // 2048 of the exponential unit. Measured: about 6.9 k cycles (2048 tokens over 32k, 16 heads of
-// 128: 770 us, 690 TFLOP/s). No unit is full: the exponentials, the unpacking and the products
+// 128: 766 us, 695 TFLOP/s). No unit is full: the exponentials, the unpacking and the products
 // each left out take 5% off, the softmax passes left out 20%; what bounds it is the latency of a
 // step's hand-offs (scores, softmax, products) with two tiles in flight, all tensor memory holds.
 //
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   // balance best but cut most tiles twice, and a range's two pieces each fill and drain the pipeline
   // and pass through the workspace. So where tiles cut into equally many parts give no part much
   // longer than a range (kCutSteps), CTAs take parts: a 1021-token prompt's 128 tiles of 1 to 8
-  // steps whole (60 -> 40 us), 64 tiles of 17 to 29 steps in two.
+  // steps whole (60 -> 41 us), 64 tiles of 17 to 31 steps in two (145 -> 129 us).
   const int n_seqs = a.b.n_seqs;
   auto scan = [&](bool tiles_only) {
     bool bad = false;
