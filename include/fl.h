@@ -596,7 +596,7 @@ FL_API fl_status fl_kv_read(const fl_kv_cache* cache, const fl_kv_batch* batch, 
  * statistics in fp32; each probability times its value scale is rounded to bf16 before the second
  * product, the output to bf16. Values up to 2^100 in magnitude are safe from overflow in the fp32
  * sums. Equal inputs give equal bits. Sequences of up to 64 rows (new tokens times query heads per
- * key/value head; 128 where n_seqs * kv_heads <= 16) take one kernel, longer chunks another: one
+ * key/value head; 256 where n_seqs * kv_heads <= 16) take one kernel, longer chunks another: one
  * launch, or two where a call of several sequences may hold both (max_new).
  *   levels     device uint8 [n_seqs][max_blocks] or NULL (every block D8)
  *   q, out     device bf16 [rows][heads][head_dim], row strides in elements (multiples of 8, at least

@@ -222,7 +222,7 @@ def test_attend_prompt_chunks(env, kvh, group, D, lens, news, levels):
 
 
 @pytest.mark.parametrize("kvh,group,D", [(1, 1, 64), (2, 2, 128), (1, 8, 64), (1, 32, 128)])
-@pytest.mark.parametrize("rows", [31, 32, 33, 127, 128, 129, 255, 256, 257, 513])
+@pytest.mark.parametrize("rows", [31, 32, 33, 127, 128, 129, 255, 256, 257, 384, 385, 511, 512, 513])
 def test_attend_row_counts(env, kvh, group, D, rows):
     """Query rows per key/value head around the kernels' limits and the tiles' sizes, alone and among others."""
     torch, fl = env

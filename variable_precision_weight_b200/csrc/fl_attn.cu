@@ -504,9 +504,9 @@ struct Ws {
 // rows costs the same however few are used, while this one reads a page again for every 16 rows.
 // Measured over 3.5-4.5k tokens, this kernel against the other: 8 sequences of 8 heads, 64 rows 47
 // and 73 against 73 and 82 us (64, 128 dims), 96 rows 63 and 102 against 76 and 84, 128 rows 80 and
-// 130 against 76 and 86; one sequence, 96 rows 21 against 42, 128 rows 31 against 58 us: its few
+// 130 against 76 and 86; one sequence, 128 rows 31 against 53, 240 rows 29 against 61 us: its few
 // tiles leave the other kernel mostly starts, ends and joins.
-static int small_rows(int n_seqs, int kv_heads) { return n_seqs * kv_heads <= 16 ? 128 : 64; }
+static int small_rows(int n_seqs, int kv_heads) { return std::min(256, std::max(64, 4096 / (n_seqs * kv_heads))); }
 
 // Rows per tile by the largest number of rows a (sequence, head) has: eight columns cost half the
 // MMAs of sixteen.
