@@ -633,3 +633,38 @@ def test_pages_beyond_32_bit_offsets(env):
         for x in (2 * h, 2 * h + 1):
             ref, tol = kv.attention(f64(q[:, x]), kk, vv, np.full(150, 4), sc, np.arange(150), np.float32(D ** -0.5), 0, 0)
             assert np.all(np.abs(f64(out[:, x].cpu().numpy()) - ref) <= tol)
+
+
+# ------------------------------------------------------------------ the calls at their edges
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_over_all_magnitudes(env, D):
+    """Rows from the smallest subnormal to the largest finite bf16: the formula's codes and scales, and
+    the values read back at eight and at four bits."""
+    torch, fl = env
+    kvh, top = 2, 0x7F7F
+    n = 262                                                               # maxima of 2^-134 .. 2^127
+    c = Case(torch, fl, [n], [n], kvh, D, seed=D, levels=(2, 4))
+    g = np.random.default_rng(D)
+    with np.errstate(over="ignore"):
+        x = (g.uniform(-1, 1, (2, n, kvh, D)) * 2.0 ** np.arange(-134, 128)[:, None, None]).astype(np.float32)
+    bits = synth.f32_to_bf16_bits(x)
+    bits = np.where((bits & 0x7FFF) > top, (bits & 0x8000) | top, bits).astype(np.uint16)
+    bits[:, -1, 0, :4] = [top, top | 0x8000, 0x7C00, 0x0001]              # the largest, both signs, and the smallest
+    any_ = g.integers(0, 1 << 16, (2, n, D)).astype(np.uint16)            # any finite pattern
+    bits[:, ::3, 1] = np.where((any_ & 0x7F80) == 0x7F80, 0x4000, any_)[:, ::3]
+    k, v = bits
+    fl.fl_kv_append(c.cache, c.batch, dev(torch, k), kvh * D, dev(torch, v), kvh * D)
+    ko, vo = (torch.zeros((n, kvh, D), dtype=torch.int16, device="cuda") for _ in "kv")
+    fl.fl_kv_read(c.cache, c.batch, c.d_levels, ko, kvh * D, vo, kvh * D)
+    fl.fl_device_status()
+    want = c.pages.copy()
+    for p in range(n):
+        for h in range(kvh):
+            (kc, ks), (vc, vs) = kv.quantise(f64(k[p, h])), kv.quantise(f64(v[p, h]))
+            kv.write_token(want[c.table[0, p // 64], h], D, p % 64, kc, ks, vc, vs)
+    assert np.array_equal(c.d_pages.cpu().numpy(), want)
+    for h in range(kvh):
+        kk, vv, _, _ = kv.gather(want, c.table[0], c.levels[0], n, D, h)
+        for got, ref in ((ko, kk), (vo, vv)):
+            assert np.array_equal(got[:, h].cpu().numpy().view(np.uint16), synth.f32_to_bf16_bits(ref.astype(np.float32)))

@@ -5,7 +5,9 @@
 // code_d = rint(127 x_d / a). 127 x_d is exact in fp32 (15 significant bits) and the division
 // is IEEE, and no quotient of two bf16 values can round across a half-integer it does not hit
 // (it lies at least 2^-17 away, fp32 rounds by at most 2^-18 below 128), so the code equals the
-// formula's in exact arithmetic, ties to even.
+// formula's in exact arithmetic, ties to even. Where 127 a could pass the largest fp32, both sides
+// of the division are taken 2^-8 times: the quotient is the same, and an element too small to
+// keep its bits has code 0 either way.
 //
 // Bound: HBM bytes (4 D read and 2 D + 8 written per token-head when appending, the reverse when
 // reading). One CTA per (sequence, touched page, key/value head): its 64 x D codes are the unit
@@ -61,7 +63,8 @@ __device__ __forceinline__ float quantise16(const uint4 (&raw)[2], uint32_t (&co
   for (int m = 1; m < LPR; m <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
   const bool finite = top < 0x7F800000u;  // NaN patterns order above infinity
   const bool live = finite && top != 0u;
-  const float a = __uint_as_float(top);
+  const bool large = top >= 0x7B800000u;  // a >= 2^120: 127 a could be infinite
+  const float a = __uint_as_float(top), f = large ? 127.f / 256.f : 127.f, div = large ? a * (1.f / 256.f) : a;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t c4 = 0;
@@ -69,7 +72,7 @@ __device__ __forceinline__ float quantise16(const uint4 (&raw)[2], uint32_t (&co
     for (int k = 0; k < 4; ++k) {
       const uint32_t ww = w[2 * i + (k >> 1)];
       const float x = __uint_as_float((k & 1) ? (ww & 0xFFFF0000u) : (ww << 16));
-      const int c = live ? __float2int_rn(__fdiv_rn(__fmul_rn(x, 127.f), a)) : 0;
+      const int c = live ? __float2int_rn(__fdiv_rn(__fmul_rn(x, f), div)) : 0;
       c4 |= (uint32_t)(c + 128) << (8 * k);
     }
     code[i] = c4;
