@@ -668,3 +668,28 @@ def test_append_over_all_magnitudes(env, D):
         kk, vv, _, _ = kv.gather(want, c.table[0], c.levels[0], n, D, h)
         for got, ref in ((ko, kk), (vo, vv)):
             assert np.array_equal(got[:, h].cpu().numpy().view(np.uint16), synth.f32_to_bf16_bits(ref.astype(np.float32)))
+
+
+def needed_blocks(n, new, width, window, sinks):
+    """Blocks that hold a key some new token sees."""
+    key, pos = np.arange(64 * width)[:, None], np.arange(n - new, n)[None, :]
+    see = key <= pos
+    if window:
+        see &= (pos - key < window) | (key < sinks)
+    return see.any(axis=1).reshape(width, 64).any(axis=1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,news", [([1500], [300]), ([1500, 900, 700], [300, 1, 5]), ([1500, 200], [1, 3])])
+@pytest.mark.parametrize("window,sinks", [(100, 0), (65, 1), (192, 64), (300, 70), (1000, 130), (64, 200), (1, 0)])
+def test_pages_outside_the_window_may_be_gone(env, D, lens, news, window, sinks):
+    """Blocks that no new token sees have no page any more: nothing is reported, nothing changes."""
+    torch, fl = env
+    c = Case(torch, fl, lens, news, 2, D, seed=window + sinks)
+    for i, (n, new) in enumerate(zip(lens, news)):
+        c.table[i, ~needed_blocks(n, new, c.width, window, sinks)] = (-1, c.num_pages)[i % 2]
+    c.upload()
+    q = c.q(8)
+    got = c.attend(q, 8, D ** -0.5, window, sinks)
+    fl.fl_device_status()
+    c.check(got, q, 8, D ** -0.5, window, sinks)

@@ -174,6 +174,12 @@ __device__ __forceinline__ Tile tile_of(const Args& a, const Geo& g, int tau) {
   return t;
 }
 __device__ __forceinline__ int step_at(const Tile& t, int p) { return p < t.sink ? p : t.first + p - t.sink; }
+// Whether some row of the tile sees a key of the block. A step's other block may have no page (behind
+// the window, between the first tokens and it): its table entry is not looked at.
+__device__ __forceinline__ bool needs(const Args& a, const Tile& t, int block) {
+  const int key0 = block * kv::kBlock;
+  return key0 <= t.pos_hi && (a.window == 0 || t.pos_lo - (key0 + kv::kBlock - 1) < a.window || key0 < a.sinks);
+}
 
 // A warp's place in the list of units; every lane holds the same.
 struct Walk {
@@ -609,7 +615,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     for (long long u = u0; u < u1 && !failed;) {
       const long long ue = min(u1, w.ia + w.t.n);
       const int p0 = (int)(u - w.ia), p1 = (int)(ue - w.ia);
-      const int blocks = w.g.s.len / kv::kBlock + (w.g.s.len % kv::kBlock != 0);
       const uint8_t* src = nullptr;
       int lv = 0;
       for (int p = p0; p < p1 && !failed; ++p) {
@@ -619,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           const int pp = p + (lane >> 1);
           if (pp < p1) {
             const int block = 2 * step_at(w.t, pp) + (lane & 1);
-            if (block < blocks) {
+            if (needs(a, w.t, block)) {
               const size_t at = (size_t)w.i * a.b.max_blocks + block;
               const int page = __ldg(a.b.table + at);
               lv = kv::level_of(a.levels, at);
