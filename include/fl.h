@@ -561,7 +561,8 @@ typedef struct {
  * change), so the kernels check them: a sequence with n_i outside 0 .. min(max_new, lens[i]), rows
  * or lens[i] out of range is left out of the call, a block whose page index is outside
  * 0 .. num_pages - 1 is not read or written (it counts as ZERO), and the next fl_device_status()
- * returns FL_ERR_ARG. Entries of the table that no listed token needs are not looked at. */
+ * returns FL_ERR_ARG. Entries of the table that no listed token needs (blocks outside every new
+ * token's window and first tokens, and blocks that a call's levels make ZERO) may hold anything. */
 typedef struct {
   const int32_t* block_table;
   const int32_t* lens;

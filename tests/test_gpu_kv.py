@@ -693,3 +693,29 @@ def test_pages_outside_the_window_may_be_gone(env, D, lens, news, window, sinks)
     got = c.attend(q, 8, D ** -0.5, window, sinks)
     fl.fl_device_status()
     c.check(got, q, 8, D ** -0.5, window, sinks)
+
+
+@pytest.mark.parametrize("new", [1, 10, 300])
+@pytest.mark.parametrize("lens", [[700], [700, 500]])
+def test_zero_blocks_need_no_page(env, lens, new):
+    """A block at level ZERO is not read, so its table entry may be anything."""
+    torch, fl = env
+    kvh, D = 2, 64
+    c = Case(torch, fl, lens, [new] * len(lens), kvh, D, seed=new, levels=(0, 2, 4))
+    c.levels[:, -1] = c.levels[:, 0] = 0
+    c.levels[:, 1] = 4
+    c.table[c.levels == 0] = -1
+    c.upload()
+    q = c.q(4)
+    got = c.attend(q, 4, 0.125)
+    fl.fl_device_status()
+    c.check(got, q, 4, 0.125)
+    ko, vo = (torch.full((c.rows, kvh * D), 55, dtype=torch.int16, device="cuda") for _ in "kv")
+    fl.fl_kv_read(c.cache, c.batch, c.d_levels, ko, kvh * D, vo, kvh * D)
+    fl.fl_device_status()
+    for i, n in enumerate(lens):
+        for h in range(kvh):
+            k, v, _, _ = kv.gather(c.pages, c.table[i], c.levels[i], n, D, h)
+            for got, ref in ((ko, k), (vo, v)):
+                have = got[c.start[i]:c.start[i + 1], h * D:(h + 1) * D].cpu().numpy().view(np.uint16)
+                assert np.array_equal(have, synth.f32_to_bf16_bits(ref[n - new:].astype(np.float32)))

@@ -628,10 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               const size_t at = (size_t)w.i * a.b.max_blocks + block;
               const int page = __ldg(a.b.table + at);
               lv = kv::level_of(a.levels, at);
-              if (page < 0 || page >= a.num_pages) {
+              if (lv > 0 && (page < 0 || page >= a.num_pages)) {
                 atomicMax(&g_error, (int)kv::kErrPage);
                 lv = 0;
-              } else {
+              } else if (lv > 0) {
                 src = a.pages + ((size_t)page * a.kv_heads + w.head) * kv::record_bytes(D);
               }
             }

@@ -83,11 +83,11 @@ __device__ __forceinline__ float quantise16(const uint4 (&raw)[2], uint32_t (&co
 struct PageJob {
   Seq s;
   int block, head, j0, j1;  // slots [j0, j1) of the block are this call's
-  int page;
+  int page, level;     // level 0: the block is ZERO or its page out of range, page is not valid
 };
 
 // The CTA's page: grid x = page touched by a sequence's new tokens, y = sequence, z = head.
-__device__ __forceinline__ bool page_job(const Batch& b, int num_pages, PageJob& jb) {
+__device__ __forceinline__ bool page_job(const Batch& b, int num_pages, const uint8_t* levels, PageJob& jb) {
   bool bad = false;
   jb.s = seq_of(b, blockIdx.y, &bad);
   jb.head = blockIdx.z;
@@ -98,10 +98,12 @@ __device__ __forceinline__ bool page_job(const Batch& b, int num_pages, PageJob&
   if (jb.block * kBlock >= jb.s.len) return false;
   jb.j0 = max(first - jb.block * kBlock, 0);
   jb.j1 = min(jb.s.len - jb.block * kBlock, kBlock);
-  jb.page = __ldg(b.table + (size_t)blockIdx.y * b.max_blocks + jb.block);
-  if (jb.page < 0 || jb.page >= num_pages) {
+  const size_t at = (size_t)blockIdx.y * b.max_blocks + jb.block;
+  jb.page = __ldg(b.table + at);
+  jb.level = level_of(levels, at);
+  if (jb.level > 0 && (jb.page < 0 || jb.page >= num_pages)) {
     if (jb.head == 0 && threadIdx.x == 0) atomicMax(&g_error, kErrPage);
-    jb.page = -1;
+    jb.level = 0;
   }
   return true;
 }
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(uint8_t* pages, int nu
   pdl_release();
   pdl_wait();
   PageJob jb;
-  if (!page_job(b, num_pages, jb) || jb.page < 0) return;
+  if (!page_job(b, num_pages, nullptr, jb) || jb.level == 0) return;
   uint8_t* rec = pages + ((size_t)jb.page * kv_heads + jb.head) * record_bytes(D);
   uint8_t* const khi = rec + kScaleBytes;
   uint8_t* const klo = khi + 2 * plane_bytes(D);
@@ -232,9 +234,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const uint8_t* pages, in
   pdl_release();
   pdl_wait();
   PageJob jb;
-  if (!page_job(b, num_pages, jb)) return;
-  const int lv = jb.page < 0 ? 0 : level_of(levels, (size_t)blockIdx.y * b.max_blocks + jb.block);
-  const uint8_t* rec = pages + ((size_t)max(jb.page, 0) * kv_heads + jb.head) * record_bytes(D);
+  if (!page_job(b, num_pages, levels, jb)) return;
+  const int lv = jb.level;
+  const uint8_t* rec = pages + ((size_t)(lv > 0 ? jb.page : 0) * kv_heads + jb.head) * record_bytes(D);
   const uint8_t* const khi = rec + kScaleBytes;
   const uint8_t* const klo = khi + 2 * plane_bytes(D);
   const uint8_t* const vhi = khi + plane_bytes(D);
