@@ -719,3 +719,46 @@ def test_zero_blocks_need_no_page(env, lens, new):
             for got, ref in ((ko, k), (vo, v)):
                 have = got[c.start[i]:c.start[i + 1], h * D:(h + 1) * D].cpu().numpy().view(np.uint16)
                 assert np.array_equal(have, synth.f32_to_bf16_bits(ref[n - new:].astype(np.float32)))
+
+
+def test_every_pending_error_is_named(env):
+    """A wait that ran out is not lost behind bad arguments, nor one kernel's report behind another's."""
+    torch, fl = env
+    fl.fl_device_status()
+
+    def pending(*calls):
+        for call in calls:
+            call()
+        with pytest.raises(fl.FlError) as e:
+            fl.fl_device_status()
+        fl.fl_device_status()                                             # every word was cleared
+        return e.value.status, str(e.value)
+
+    def case(news, page=False, seq=False):
+        c = Case(torch, fl, [700, 400], news, 2, 64, seed=6)
+        if page:
+            c.table[0, 0] = c.num_pages
+        if seq:
+            c.lens[1] = -1
+        c.upload()
+        return c
+
+    def attend(c):
+        ws, n = c.workspace(4)
+        q = torch.zeros((c.rows, 256), dtype=torch.int16, device="cuda")
+        fl.fl_attn_paged(c.cache, c.batch, None, q, 256, 4, 0.1, 0, 0, q, 256, ws, n)
+        return ws
+
+    def read(c):
+        x = torch.zeros((c.rows, 128), dtype=torch.int16, device="cuda")
+        fl.fl_kv_read(c.cache, c.batch, None, x, 128, torch.zeros_like(x), 128)
+
+    for news in ([2, 2], [300, 300]):
+        status, text = pending(fl.fl_selftest_wait_timeout, lambda: attend(case(news, page=True)))
+        assert status == -7 and "self-test" in text and "attention: a page" in text, text
+        status, text = pending(lambda: attend(case(news, page=True, seq=True)))
+        assert status == -1 and "attention: a page" in text and "attention: a sequence" in text, text
+        status, text = pending(lambda: attend(case(news, page=True)), lambda: read(case([2, 2], seq=True)))
+        assert status == -1 and "attention: a page" in text and "cache append or read: a sequence" in text, text
+    status, text = pending(lambda: attend(case([2, 2], page=True)), lambda: attend(case([300, 300], seq=True)))
+    assert status == -1 and "attention: a page" in text and "attention: a sequence" in text, text

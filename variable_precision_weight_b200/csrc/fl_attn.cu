@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     items = __reduce_add_sync(0xffffffffu, min(items, 1 << 20));
     if (lane == 0 && items > 0) atomicAdd(&s_items, items);
-    if (bad && blockIdx.x == 0) atomicMax(&g_error, (int)kv::kErrSeq);
+    if (bad && blockIdx.x == 0) atomicOr(&g_error, (int)kv::kErrSeq);
     inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         lv = kv::level_of(a.levels, at);
         const int page = __ldg(a.b.table + at);
         if (lv > 0 && (page < 0 || page >= a.num_pages)) {
-          atomicMax(&g_error, (int)kv::kErrPage);
+          atomicOr(&g_error, (int)kv::kErrPage);
           lv = 0;
         } else if (lv > 0) {
           src = a.pages + ((size_t)page * a.kv_heads + item / tiles) * C::kRec;
@@ -311,10 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         __syncwarp();
       }
     }
-    if (failed && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+    if (failed && lane == 0) atomicOr(&g_error, (int)kv::kErrWait);
     // no copy may still be landing when the CTA exits
     for (int k = max(0, issued - NS); k < issued; ++k)
-      if (!mbar_wait(&full_bar[k % NS], (uint32_t)((k / NS) & 1)) && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+      if (!mbar_wait(&full_bar[k % NS], (uint32_t)((k / NS) & 1)) && lane == 0) atomicOr(&g_error, (int)kv::kErrWait);
     return;
   }
 
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       // issued after it and NS >= kWarps), the parity is this lap's own.
       if (!__all_sync(0xffffffffu, (lap == 0 || mbar_wait(&empty_bar[s], (uint32_t)((lap - 1) & 1))) &&
                                        mbar_wait(&full_bar[s], (uint32_t)(lap & 1)))) {
-        if (lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+        if (lane == 0) atomicOr(&g_error, (int)kv::kErrWait);
         failed = true;
         break;
       }

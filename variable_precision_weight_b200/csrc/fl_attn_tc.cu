@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) atomicMax(&s_longest, longest);
-    if (bad && blockIdx.x == 0) atomicMax(&g_error, (int)kv::kErrSeq);
+    if (bad && blockIdx.x == 0) atomicOr(&g_error, (int)kv::kErrSeq);
     __syncthreads();
     if (warp == 0) {
       const int per = (n_seqs + 31) / 32, i0 = min(lane * per, n_seqs), i1 = min(i0 + per, n_seqs);
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               const int page = __ldg(a.b.table + at);
               lv = kv::level_of(a.levels, at);
               if (lv > 0 && (page < 0 || page >= a.num_pages)) {
-                atomicMax(&g_error, (int)kv::kErrPage);
+                atomicOr(&g_error, (int)kv::kErrPage);
                 lv = 0;
               } else if (lv > 0) {
                 src = a.pages + ((size_t)page * a.kv_heads + w.head) * kv::record_bytes(D);
@@ -652,10 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       u = ue;
       if (u < u1) advance();
     }
-    if (failed && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+    if (failed && lane == 0) atomicOr(&g_error, (int)kv::kErrWait);
     // no copy may still be landing when the CTA exits
     for (int k = max(0, unit - NR); k < unit; ++k)
-      if (!mbar_wait(&raw_full[k % NR], (uint32_t)((k / NR) & 1)) && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+      if (!mbar_wait(&raw_full[k % NR], (uint32_t)((k / NR) & 1)) && lane == 0) atomicOr(&g_error, (int)kv::kErrWait);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA issue: one thread
     if (elect_one()) {
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       // every MMA is complete before TMEM is freed: the last commit tracks all of them
       if (ok && base > 0) ok = mbar_wait(&op_empty[(base - 1) % NS], (uint32_t)(((base - 1) / NS) & 1));
-      if (!ok) atomicMax(&g_error, (int)kv::kErrWait);
+      if (!ok) atomicOr(&g_error, (int)kv::kErrWait);
     }
     __syncwarp();
   }
@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         u = ue;
         if (u < u1) advance();
       }
-      if (failed && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+      if (failed && lane == 0) atomicOr(&g_error, (int)kv::kErrWait);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       u = ue;
       if (u < u1) advance();
     }
-    if (!ok && lane == 0) atomicMax(&g_error, (int)kv::kErrWait);
+    if (!ok && lane == 0) atomicOr(&g_error, (int)kv::kErrWait);
   }
 
   fence_before();

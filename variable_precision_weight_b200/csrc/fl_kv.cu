@@ -91,7 +91,7 @@ __device__ __forceinline__ bool page_job(const Batch& b, int num_pages, const ui
   bool bad = false;
   jb.s = seq_of(b, blockIdx.y, &bad);
   jb.head = blockIdx.z;
-  if (bad && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicMax(&g_error, kErrSeq);
+  if (bad && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicOr(&g_error, kErrSeq);
   if (jb.s.n == 0) return false;
   const int first = jb.s.len - jb.s.n;
   jb.block = first / kBlock + (int)blockIdx.x;
@@ -102,7 +102,7 @@ __device__ __forceinline__ bool page_job(const Batch& b, int num_pages, const ui
   jb.page = __ldg(b.table + at);
   jb.level = level_of(levels, at);
   if (jb.level > 0 && (jb.page < 0 || jb.page >= num_pages)) {
-    if (jb.head == 0 && threadIdx.x == 0) atomicMax(&g_error, kErrPage);
+    if (jb.head == 0 && threadIdx.x == 0) atomicOr(&g_error, kErrPage);
     jb.level = 0;
   }
   return true;

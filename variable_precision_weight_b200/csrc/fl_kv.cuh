@@ -28,7 +28,7 @@ struct Batch {
   int n_seqs, max_blocks, rows, max_new;
 };
 
-enum : int { kErrSeq = 1, kErrPage = 2, kErrWait = 3 };  // error words; the largest seen is kept
+enum : int { kErrSeq = 1, kErrPage = 2, kErrWait = 4 };  // bits of an error word
 
 struct Seq {
   int row0, n, len;  // first row, new tokens, cached tokens; n = 0: nothing to do

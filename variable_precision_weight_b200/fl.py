@@ -198,7 +198,8 @@ def fl_level_map(xy, nblocks: int, centers, radii, nlenses: int, params: fl_lens
 
 
 def fl_device_status() -> None:
-    """Raises FlError(FL_ERR_TIMEOUT) if a kernel's bounded wait ran out since the last call."""
+    """Raises FlError(FL_ERR_TIMEOUT) if a kernel's bounded wait ran out since the last call, else
+    FlError(FL_ERR_ARG) if a kernel found bad device data; the message names every pending error."""
     _check(_lib.fl_device_status())
 
 
