@@ -595,15 +595,15 @@ FL_API fl_status fl_kv_read(const fl_kv_cache* cache, const fl_kv_batch* batch, 
  * A key that a query does not see has no influence on its output, whatever its values (NaN among
  * them). Arithmetic: products of bf16 queries with exact codes, accumulated in fp32; the softmax
  * statistics in fp32; each probability times its value scale is rounded to bf16 before the second
- * product, the output to bf16. Values up to 2^100 in magnitude are safe from overflow in the fp32
- * sums. Equal inputs give equal bits. Sequences of up to 64 rows (new tokens times query heads per
+ * product, the output to bf16. Scores have to fit fp32 with room (|z_j| and |scale k| below 2^115,
+ * |q| and |v| below 2^90); beyond that a row may come out NaN. Equal inputs give equal bits. Sequences of up to 64 rows (new tokens times query heads per
  * key/value head; 256 where n_seqs * kv_heads <= 16) take one kernel, longer chunks another: one
  * launch, or two where a call of several sequences may hold both (max_new).
  *   levels     device uint8 [n_seqs][max_blocks] or NULL (every block D8)
  *   q, out     device bf16 [rows][heads][head_dim], row strides in elements (multiples of 8, at least
  *              heads * head_dim), 16-byte aligned; out may be q
  *   heads      a multiple of kv_heads, at most FL_ATTN_MAX_GROUP * kv_heads
- *   scale      finite;  window >= 0;  sinks >= 0 (read only with a window)
+ *   scale      at most 2^117 in magnitude;  window >= 0;  sinks >= 0 (read only with a window)
  *   workspace  at least fl_attn_workspace_bytes(n_seqs, heads, kv_heads, head_dim, max_new) bytes
  *              (up to 5 MB for short calls, 20 or 40 MB more for chunks), 16-byte aligned, ZERO-FILLED before its first use; every completed call leaves its
  *              counters at zero. Calls that share a workspace must not overlap on the GPU.

@@ -762,3 +762,18 @@ def test_every_pending_error_is_named(env):
         assert status == -1 and "attention: a page" in text and "cache append or read: a sequence" in text, text
     status, text = pending(lambda: attend(case([2, 2], page=True)), lambda: attend(case([300, 300], seq=True)))
     assert status == -1 and "attention: a page" in text and "attention: a sequence" in text, text
+
+
+@pytest.mark.parametrize("new", [2, 300])
+@pytest.mark.parametrize("exp", [-117, 117])
+def test_largest_scales(env, new, exp):
+    """scale at the largest that is taken, over keys as small; and the reverse."""
+    torch, fl = env
+    c = Case(torch, fl, [500], [new], 2, 64, seed=5, levels=(2, 4))
+    sc = c.pages[:, :, :512].view(np.float32).reshape(c.num_pages, 2, 2, 64)
+    sc[:, :, 0] *= np.float32(2.0) ** -exp
+    c.upload()
+    q = c.q(4, 0.1)
+    got = c.attend(q, 4, 2.0 ** exp)
+    fl.fl_device_status()
+    c.check(got, q, 4, 2.0 ** exp)

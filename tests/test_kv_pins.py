@@ -142,3 +142,10 @@ def test_refusals(fl):
         assert _status(fl, lambda kw=kw: attn(**kw)) == SHAPE, kw
     for kw in (dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1), dict(sinks=-1)):
         assert _status(fl, lambda kw=kw: attn(**kw)) == ARG, kw
+
+
+@pytest.mark.parametrize("scale", [1.7e35, -1.7e35, 2e38, 3.4e38, -3.4e38])
+def test_scale_beyond_the_kernels_range_is_refused(fl, scale):
+    """Above 2^117 (1.66e35) the codes' factor times scale log2(e) is no longer finite in fp32."""
+    c, b = fl.kv_cache(16, 4, 2, 64), fl.kv_batch(16, 16, 16, 2, 3, 8, 4)
+    assert _status(fl, lambda: fl.fl_attn_paged(c, b, None, 16, 128, 2, scale, 0, 0, 16, 128, 16, 1 << 30, 0)) == -1

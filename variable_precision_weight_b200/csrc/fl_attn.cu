@@ -23,6 +23,8 @@
 //  * At the end of an item (sequence, head, row tile) the warps' states join in shared memory. An
 //    item cut by a range boundary leaves partials in the workspace, joined by the CTA that arrives
 //    last, in CTA order, so results do not depend on the order of arrival.
+#include <math.h>
+
 #include <algorithm>
 
 #include "fl_attn.cuh"
@@ -569,7 +571,8 @@ extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* 
                 FL_ATTN_MAX_GROUP);
   if (fl_status s = kv::check_rows(what, "q", q, q_stride, heads * D)) return s;
   if (fl_status s = kv::check_rows(what, "out", out, out_stride, heads * D)) return s;
-  if (!(scale - scale == 0.f)) return fail(FL_ERR_ARG, "%s: scale is not finite", what);
+  // 2^117: scale log2(e) times the codes' factor (2^10 at D4) is still finite in fp32
+  if (!(fabsf(scale) <= 0x1p117f)) return fail(FL_ERR_ARG, "%s: scale=%g (at most 2^117 in magnitude)", what, scale);
   if (window < 0 || sinks < 0) return fail(FL_ERR_ARG, "%s: window=%d, sinks=%d (>= 0)", what, window, sinks);
   const int nsm = std::min(device_sm_count(), attn::kMaxGrid);
   if (nsm <= 0) return fail(FL_ERR_CUDA, "%s: no CUDA device", what);
