@@ -777,3 +777,26 @@ def test_largest_scales(env, new, exp):
     got = c.attend(q, 4, 2.0 ** exp)
     fl.fl_device_status()
     c.check(got, q, 4, 2.0 ** exp)
+
+
+def attend_counted(c, q, heads, scale, *rest):
+    """c.attend, and the counters of both kernels are zero behind it."""
+    ws, n = c.workspace(heads)
+    got = c.attend(q, heads, scale, *rest, ws=(ws, n))
+    assert not ws[:4096].any()
+    return got
+
+
+def test_half_tiles_before_whole_tiles(env):
+    """Equal ranges in which tiles of at most 128 rows (one of the kernel's two halves has nothing to do for many
+    steps) are followed by tiles of 129 to 256."""
+    torch, fl = env
+    kvh, D = 16, 64
+    lens, news = [1300, 260] * 5, [100, 200] * 5
+    c = Case(torch, fl, lens, news, kvh, D, seed=31, levels=(2, 4))
+    q = c.q(kvh)
+    got = attend_counted(c, q, kvh, 0.125)
+    fl.fl_device_status()
+    c.check(got, q, kvh, 0.125, skip=range(3, 9))
+    for _ in range(3):
+        assert np.array_equal(attend_counted(c, q, kvh, 0.125), got)

@@ -848,8 +848,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         float l[4] = {0.f, 0.f, 0.f, 0.f};
         for (int j = 0; j < n && ok; ++j, ++cnt) {
           const int sr = (step + j) % kScaleRing, key0 = kStep * step_at(w.t, p0 + j);
-          ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[sr], (uint32_t)(((step + j) / kScaleRing) & 1)) &&
-                                           mbar_wait(&s_full[t], (uint32_t)(cnt & 1)));
+          // The scores first: a half that skipped tiles without rows may be laps ahead of sc_full, whose
+          // parity alone would then fall through on an older lap. Scores of this step mean that every
+          // unpacking warp has passed its keys, so sc_full is in this step's lap; and it stays there,
+          // since the keys kScaleRing steps on need an operand slot that frees after this half's P.
+          ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)(cnt & 1)) &&
+                                           mbar_wait(&sc_full[sr], (uint32_t)(((step + j) / kScaleRing) & 1)));
           if (!ok) break;
           fence_after();
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
