@@ -290,10 +290,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         const size_t at = (size_t)i * a.b.max_blocks + block;
         lv = kv::level_of(a.levels, at);
         const int page = __ldg(a.b.table + at);
-        if (lv > 0 && (page < 0 || page >= a.num_pages)) {
-          atomicOr(&g_error, (int)kv::kErrPage);
+        if (page < 0 || page >= a.num_pages) {  // a ZERO block's entry may be anything
+          if (lv > 0) atomicOr(&g_error, (int)kv::kErrPage);
           lv = 0;
-        } else if (lv > 0) {
+        } else {
           src = a.pages + ((size_t)page * a.kv_heads + item / tiles) * C::kRec;
         }
       }
