@@ -628,10 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               const size_t at = (size_t)w.i * a.b.max_blocks + block;
               const int page = __ldg(a.b.table + at);
               lv = kv::level_of(a.levels, at);
-              if (lv > 0 && (page < 0 || page >= a.num_pages)) {
-                atomicOr(&g_error, (int)kv::kErrPage);
+              if (page < 0 || page >= a.num_pages) {  // a ZERO block's entry may be anything
+                if (lv > 0) atomicOr(&g_error, (int)kv::kErrPage);
                 lv = 0;
-              } else if (lv > 0) {
+              } else {
                 src = a.pages + ((size_t)page * a.kv_heads + w.head) * kv::record_bytes(D);
               }
             }
@@ -846,14 +846,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const int phi = w.g.pos0 + (w.t.r0 + min(kTile * t + kTile, w.t.nrows) - 1) / a.group;
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         float l[4] = {0.f, 0.f, 0.f, 0.f};
+        // A half that skipped tiles without rows may be laps ahead of sc_full, whose parity alone would
+        // then fall through on an older lap. The first step's scores mean that every unpacking warp
+        // has passed its keys, so from there on the barriers are in the laps that are waited for; and
+        // they stay: the keys kScaleRing steps on need an operand slot that frees after this half's P.
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)(cnt & 1)));
         for (int j = 0; j < n && ok; ++j, ++cnt) {
           const int sr = (step + j) % kScaleRing, key0 = kStep * step_at(w.t, p0 + j);
-          // The scores first: a half that skipped tiles without rows may be laps ahead of sc_full, whose
-          // parity alone would then fall through on an older lap. Scores of this step mean that every
-          // unpacking warp has passed its keys, so sc_full is in this step's lap; and it stays there,
-          // since the keys kScaleRing steps on need an operand slot that frees after this half's P.
-          ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)(cnt & 1)) &&
-                                           mbar_wait(&sc_full[sr], (uint32_t)(((step + j) / kScaleRing) & 1)));
+          ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[sr], (uint32_t)(((step + j) / kScaleRing) & 1)) &&
+                                           mbar_wait(&s_full[t], (uint32_t)(cnt & 1)));
           if (!ok) break;
           fence_after();
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
