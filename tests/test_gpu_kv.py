@@ -800,3 +800,142 @@ def test_half_tiles_before_whole_tiles(env):
     c.check(got, q, kvh, 0.125, skip=range(3, 9))
     for _ in range(3):
         assert np.array_equal(attend_counted(c, q, kvh, 0.125), got)
+
+
+@pytest.mark.parametrize("kvh,group,D,lens,news", [
+    (1, 1, 64, [9000], [300]), (2, 2, 128, [6000], [140]), (2, 4, 64, [5000, 70], [100, 1]), (8, 1, 64, [3000, 900], [290, 257]),
+    (8, 1, 64, [400 + 97 * i for i in range(20)], [63 + i for i in range(20)])])
+def test_joined_chunks_leave_the_counters_at_zero(env, kvh, group, D, lens, news):
+    """Tiles cut into parts, and cut anywhere by equal ranges, on the chunk kernel (more than 256 rows in some sequence)."""
+    torch, fl = env
+    heads = kvh * group
+    c = Case(torch, fl, lens, news, kvh, D, seed=sum(lens), levels=(2, 4))
+    q = c.q(heads)
+    for window, sinks in ((0, 0), (700, 70)):
+        got = attend_counted(c, q, heads, 0.1, window, sinks)
+        fl.fl_device_status()
+        c.check(got, q, heads, 0.1, window, sinks, skip=range(2, len(lens) - 1))
+        assert np.array_equal(attend_counted(c, q, heads, 0.1, window, sinks), got)
+
+
+@pytest.mark.parametrize("n_seqs", [1, 3])
+def test_captured_chunks_follow_device_lengths(env, n_seqs):
+    """The chunk kernel (alone, and behind the other) captured once; replayed after lens, rows and table change."""
+    torch, fl = env
+    kvh, heads, D, rows, width = 2, 4, 64, 640, 12
+    lens, news = [700, 300, 100][:n_seqs], [300, 290, 1][:n_seqs]
+    c = Case(torch, fl, lens, news, kvh, D, seed=6, rows=rows, max_new=300, width=width, spare=30)
+    q = c.q(heads)
+    w = heads * D
+    d_q, d_out = dev(torch, q), torch.full((rows, heads, D), 77, dtype=torch.int16, device="cuda")
+    ws, n = c.workspace(heads)
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        fl.fl_attn_paged(c.cache, c.batch, None, d_q, w, heads, 0.1, 0, 0, d_out, w, ws, n, st)
+        st.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            fl.fl_attn_paged(c.cache, c.batch, None, d_q, w, heads, 0.1, 0, 0, d_out, w, ws, n, st)
+    for r, (lens, news) in enumerate((([700, 300, 100], [300, 290, 1]), ([300, 768, 384], [300, 40, 300]), ([1, 0, 130], [1, 0, 0]),
+                                      ([650, 129, 64], [33, 129, 64]), ([0, 0, 0], [0, 0, 0]), ([768, 5, 600], [257, 5, 70]))):
+        c.lens, c.news = lens[:n_seqs], news[:n_seqs]
+        c.start = np.concatenate([[0], np.cumsum(c.news)]).astype(np.int32)
+        order = np.random.default_rng(r).permutation(c.num_pages)
+        c.table[:] = -5
+        at = 0
+        for i, x in enumerate(c.lens):
+            c.table[i, :-(-x // 64)] = order[at:at + -(-x // 64)]
+            at += -(-x // 64)
+        c.d_table.copy_(torch.from_numpy(c.table))
+        c.d_lens.copy_(torch.tensor(c.lens, dtype=torch.int32))
+        c.d_start.copy_(torch.from_numpy(c.start))
+        d_out.fill_(77)
+        graph.replay()
+        fl.fl_device_status()
+        assert not ws[:4096].any()
+        got = d_out.cpu().numpy().view(np.uint16)
+        c.check(got, q, heads, 0.1)
+        c.untouched(got)
+    del graph
+
+
+def test_bad_device_data_of_chunks_is_reported(env):
+    """What test_bad_device_data_is_reported asks, of sequences that the chunk kernel takes."""
+    torch, fl = env
+    good = ([700, 400, 450], [0, 300, 305, 600])
+    c = Case(torch, fl, good[0], [300, 5, 295], 2, 64, seed=14)
+    q = c.q(4)
+    c.check(attend_counted(c, q, 4, 0.1), q, 4, 0.1)
+    fl.fl_device_status()
+    for seq, block, page in ((0, 3, c.num_pages), (2, 0, -1), (2, 7, 2 ** 31 - 1)):
+        keep = int(c.table[seq, block])
+        c.table[seq, block] = page
+        c.upload()
+        got = attend_counted(c, q, 4, 0.1)
+        with pytest.raises(fl.FlError) as e:
+            fl.fl_device_status()
+        assert e.value.status == -1 and "page" in str(e.value)
+        c.check(got, q, 4, 0.1)                                   # the reference reads that block as ZERO
+        c.table[seq, block] = keep
+    c.upload()
+    for lens, start in (([-1, 400, 450], good[1]), ([64 * c.width + 1, 400, 450], good[1]), ([299, 400, 450], good[1]),
+                        ([700, 400, 2 ** 31 - 1], good[1]), (good[0], [0, 300, 305, 601]), (good[0], [0, 300, 299, 594]),
+                        ([700, 400, 294], good[1])):
+        c.d_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        c.d_start.copy_(torch.tensor(start, dtype=torch.int32))
+        got = attend_counted(c, q, 4, 0.1)
+        with pytest.raises(fl.FlError) as e:
+            fl.fl_device_status()
+        assert e.value.status == -1 and "sequence" in str(e.value), (lens, start)
+        fl.fl_device_status()
+        bad = [not (0 <= lens[i] <= 64 * c.width and 0 <= start[i] <= start[i + 1] <= 600 and
+                    start[i + 1] - start[i] <= min(300, lens[i])) for i in range(3)]
+        assert any(bad)
+        for i in range(3):
+            if start[i:i + 2] != good[1][i:i + 2]:
+                continue
+            if bad[i]:
+                assert np.all(got[good[1][i]:good[1][i + 1]] == 77)
+            else:
+                c.check(got, q, 4, 0.1, skip=[x for x in range(3) if x != i])
+
+
+def test_append_leaves_bad_blocks_and_sequences_out(env):
+    """A page index or length out of range: that block or sequence is not written, all others are, byte for byte."""
+    torch, fl = env
+    kvh, D = 2, 64
+    for what in ("page", "sequence"):
+        c = Case(torch, fl, [200, 100, 130], [80, 100, 2], kvh, D, seed=4)
+        if what == "page":
+            c.table[0, 2] = c.num_pages
+        else:
+            c.lens[2] = 64 * c.width + 1
+        c.upload()
+        k, v = (synth.bf16_normal((c.rows, kvh, D), 4, x) for x in (1, 2))
+        fl.fl_kv_append(c.cache, c.batch, dev(torch, k), kvh * D, dev(torch, v), kvh * D)
+        with pytest.raises(fl.FlError) as e:
+            fl.fl_device_status()
+        assert e.value.status == -1 and what in str(e.value)
+        want = c.pages.copy()
+        for i, (n, new) in enumerate(zip(c.lens, c.news)):
+            for x in range(new):
+                p, r = n - new + x, c.start[i] + x
+                if n > 64 * c.width or c.table[i, p // 64] >= c.num_pages:
+                    continue
+                for h in range(kvh):
+                    (kc, ks), (vc, vs) = kv.quantise(f64(k[r, h])), kv.quantise(f64(v[r, h]))
+                    kv.write_token(want[c.table[i, p // 64], h], D, p % 64, kc, ks, vc, vs)
+        assert np.array_equal(c.d_pages.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("kvh,n_seqs,rows", [(8, 3, 169), (8, 3, 170), (8, 3, 171), (8, 4, 127), (8, 4, 128), (8, 4, 129),
+                                             (4, 5, 204), (4, 5, 205), (9, 7, 64), (9, 7, 65), (9, 7, 66)])
+def test_attend_row_counts_of_several_sequences(env, kvh, n_seqs, rows):
+    """Row counts around the kernels' limit where it lies between 64 and 256."""
+    torch, fl = env
+    c = Case(torch, fl, [rows + 50 + 40 * i for i in range(n_seqs)], [rows, 1] + [rows - 3 * i for i in range(2, n_seqs)], kvh, 64,
+             seed=rows, levels=(2, 4, 4, 0))
+    q = c.q(kvh)
+    got = attend_counted(c, q, kvh, 0.125)
+    fl.fl_device_status()
+    c.check(got, q, kvh, 0.125, skip=range(3, n_seqs))
