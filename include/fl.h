@@ -596,17 +596,23 @@ FL_API fl_status fl_kv_read(const fl_kv_cache* cache, const fl_kv_batch* batch, 
  * them). Arithmetic: products of bf16 queries with exact codes, accumulated in fp32; the softmax
  * statistics in fp32; each probability times its value scale is rounded to bf16 before the second
  * product, the output to bf16. Scores have to fit fp32 with room (|z_j| and |scale k| below 2^115,
- * |q| and |v| below 2^90); beyond that a row may come out NaN. Equal inputs give equal bits. Sequences of up to 64 rows (new tokens times query heads per
- * key/value head; 256 where n_seqs * kv_heads <= 16) take one kernel, longer chunks another: one
- * launch, or two where a call of several sequences may hold both (max_new).
+ * |q| and |v| below 2^90); beyond that a row may come out NaN. Equal inputs give equal bits.
+ * Two kernels share the work: sequences of up to 64 rows (new tokens times query heads per key/value
+ * head) take one, those of more than 256 the other, and those between the one that is faster for
+ * their rows and visible blocks; a single sequence whose max_new allows more than 256 rows takes the
+ * second however many rows it has. One launch where max_new, max_blocks and the window leave one
+ * kernel, else two. Calls whose work passes 2^31 - 1 units of 16 rows by one block in a sequence
+ * (or in an SM's share) are refused (FL_ERR_SHAPE).
  *   levels     device uint8 [n_seqs][max_blocks] or NULL (every block D8)
  *   q, out     device bf16 [rows][heads][head_dim], row strides in elements (multiples of 8, at least
  *              heads * head_dim), 16-byte aligned; out may be q
  *   heads      a multiple of kv_heads, at most FL_ATTN_MAX_GROUP * kv_heads
  *   scale      at most 2^117 in magnitude;  window >= 0;  sinks >= 0 (read only with a window)
  *   workspace  at least fl_attn_workspace_bytes(n_seqs, heads, kv_heads, head_dim, max_new) bytes
- *              (up to 5 MB for short calls, 20 or 40 MB more for chunks), 16-byte aligned, ZERO-FILLED before its first use; every completed call leaves its
- *              counters at zero. Calls that share a workspace must not overlap on the GPU.
+ *              (at most 2.5 MB for 148 SMs; 20 or 39 MB more, for head_dim 64 or 128, where max_new
+ *              allows more than 64 rows), 16-byte aligned, ZERO-FILLED before its first use and
+ *              after an FL_ERR_TIMEOUT; every completed call leaves its counters at zero. Calls that
+ *              share a workspace must not overlap on the GPU.
  * fl_attn_workspace_bytes is 0 for an invalid shape (and without a device). */
 FL_API size_t fl_attn_workspace_bytes(int n_seqs, int heads, int kv_heads, int head_dim, int max_new);
 

@@ -939,3 +939,31 @@ def test_attend_row_counts_of_several_sequences(env, kvh, n_seqs, rows):
     got = attend_counted(c, q, kvh, 0.125)
     fl.fl_device_status()
     c.check(got, q, kvh, 0.125, skip=range(3, n_seqs))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 4)])
+def test_sequences_shared_by_both_kernels(env, D, window, sinks):
+    """One call whose sequences of 65 to 256 rows divide by how many blocks they see; and a table wider than they need."""
+    torch, fl = env
+    kvh = 8
+    lens, news = [300, 620, 900, 1500, 230, 2100, 66, 64], [200, 130, 256, 70, 65, 256, 64, 64]
+    for width in (None, 4096):
+        c = Case(torch, fl, lens, news, kvh, D, seed=D + window, levels=(2, 4), rows=sum(news) + 3, width=width)
+        q = c.q(kvh)
+        got = attend_counted(c, q, kvh, 0.1, window, sinks)
+        fl.fl_device_status()
+        c.check(got, q, kvh, 0.1, window, sinks, skip=(1, 4, 6))
+        c.untouched(got)
+        assert np.array_equal(attend_counted(c, q, kvh, 0.1, window, sinks), got)
+
+
+@pytest.mark.parametrize("n,new,width", [(2000, 128, None), (300, 128, 40000), (20000, 256, None), (30000, 100, 469), (90, 65, 30000)])
+def test_one_sequence_between_the_kernels(env, n, new, width):
+    """One sequence of 65 to 256 rows: short and long contexts, under tables that allow more."""
+    torch, fl = env
+    c = Case(torch, fl, [n], [new], 4, 64, seed=n, levels=(2, 4), width=width)
+    q = c.q(4)
+    got = attend_counted(c, q, 4, 0.125)
+    fl.fl_device_status()
+    c.check(got, q, 4, 0.125)

@@ -502,25 +502,35 @@ struct Ws {
   size_t tickets, tc_tickets, partial, tc_partial, total;
 };
 
-// Sequences with more rows (new tokens x group) than this take the tcgen05 kernel, whose tile of 256
-// rows costs the same however few are used, while this one reads a page again for every 16 rows.
-// Measured over 3.5-4.5k tokens, this kernel against the other: 8 sequences of 8 heads, 64 rows 47
-// and 73 against 73 and 82 us (64, 128 dims), 96 rows 63 and 102 against 76 and 84, 128 rows 80 and
-// 130 against 76 and 86; one sequence, 128 rows 31 against 53, 240 rows 29 against 61 us: its few
-// tiles leave the other kernel mostly starts, ends and joins.
-static int small_rows(int n_seqs, int kv_heads) { return std::min(256, std::max(64, 4096 / (n_seqs * kv_heads))); }
+// Which kernel takes a sequence: this one reads and unpacks a page again for every 16 rows; the chunk
+// kernel does it once for 256, but starts, ends and joins its tiles at 30-50 us more a call. With
+// r rows that see p pages, in a call of nk (sequence, head) pairs, this kernel's extra time grows as
+// (r - 56) p nk (at 64 rows both read at the same rate), and what it saves shrinks as nk grows, since
+// many tiles need few joins. Measured, this kernel against the other, us, eight heads:
+//   D = 128   1 x 4k: 128 rows 30, 56; 256 rows 40, 74    1 x 32k: 96 rows 86, 93; 256 rows 192, 132
+//             2 x 100k: 64 rows 304, 299; 256 rows 1191, 400    4 x 4k: 128 rows 68, 67
+//             8 x 1k: 96 rows 44, 48; 256 rows 88, 64    8 x 4k: 64 rows 68, 87; 128 rows 121, 92
+//   D = 64    1 x 4k: 256 rows 30, 64    1 x 32k: 128 rows 79, 82; 256 rows 144, 110
+//             2 x 100k: 64 rows 224, 266; 256 rows 861, 335    8 x 4k: 96 rows 65, 74; 128 rows 81, 75
+// Over 306 such shapes (1k to 100k tokens, both depths, groups of 2, 4 and 8) the chosen kernel is
+// within 12% of the better one, 0.2% on average. Each sequence's own pages count, not the table's
+// width, so both kernels are launched where the call's bounds leave the choice open: 5 to 7 us, for
+// instance 28 instead of 22 us for 128 rows over 1,000 tokens under a table of 131,072.
+static long long chunk_budget(int D, long long nk) {
+  return D == 64 ? std::min(400000ll, 12000000 / nk) / nk : std::min(280000ll, 5000000 / nk) / nk;
+}
 
 // Rows per tile by the largest number of rows a (sequence, head) has: eight columns cost half the
 // MMAs of sixteen.
 static int row_tiles(long long max_rows) { return max_rows <= 8 ? 1 : 2; }
 
-static Ws ws_layout(int nsm, int D, long long max_rows, int small) {
+static Ws ws_layout(int nsm, int D, long long max_rows, bool chunks) {
   Ws w;
   w.tickets = 0;
   w.tc_tickets = (size_t)kMaxGrid * 4;
   w.partial = 2 * (size_t)kMaxGrid * 4;
   w.tc_partial = w.partial + (size_t)nsm * 2 * (8 * row_tiles(max_rows)) * (D + 2) * 4;
-  w.total = w.tc_partial + (max_rows > small ? attn_tc::partial_bytes(D, nsm) : 0);
+  w.total = w.tc_partial + (chunks ? attn_tc::partial_bytes(D, nsm) : 0);
   return w;
 }
 
@@ -555,7 +565,8 @@ extern "C" size_t fl_attn_workspace_bytes(int n_seqs, int heads, int kv_heads, i
   using namespace fl;
   const int nsm = std::min(device_sm_count(), attn::kMaxGrid);
   if (nsm <= 0 || !attn::shape_ok(n_seqs, heads, kv_heads, head_dim, max_new)) return 0;
-  return attn::ws_layout(nsm, head_dim, (long long)max_new * (heads / kv_heads), attn::small_rows(n_seqs, kv_heads)).total;
+  const long long max_rows = (long long)max_new * (heads / kv_heads);
+  return attn::ws_layout(nsm, head_dim, max_rows, max_rows > attn::kShortRows).total;
 }
 
 extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* batch, const uint8_t* levels,
@@ -582,8 +593,13 @@ extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* 
   if (units > 2147483647.0 || units * batch->n_seqs / nsm > 2147483647.0)
     return fail(FL_ERR_SHAPE, "%s: max_new=%d over max_blocks=%d is too large for one call", what, batch->max_new,
                 batch->max_blocks);
-  const int small = attn::small_rows(batch->n_seqs, Hkv);
-  const attn::Ws wl = attn::ws_layout(nsm, D, max_rows, small);
+  // what a sequence of this call can ask for at most
+  long long pages = batch->max_blocks;
+  if (window > 0)
+    pages = std::min(pages, ((long long)window + batch->max_new + 62) / kv::kBlock + 1 + ((long long)sinks + 63) / kv::kBlock);
+  const long long budget = attn::chunk_budget(D, (long long)batch->n_seqs * Hkv);
+  const bool chunks = attn::chunk_takes(max_rows, pages, budget);
+  const attn::Ws wl = attn::ws_layout(nsm, D, max_rows, chunks);
   if (!workspace || workspace_bytes < wl.total)
     return fail(FL_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", what, workspace ? workspace_bytes : (size_t)0,
                 wl.total);
@@ -604,21 +620,20 @@ extern "C" fl_status fl_attn_paged(const fl_kv_cache* cache, const fl_kv_batch* 
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.window = window;
   a.sinks = sinks;
-  a.min_rows = 1;
-  a.max_rows = small;
+  // One sequence that may be a long chunk: the chunk kernel takes it whatever its length turns out to
+  // be, and a prompt saves the other launch (about 5 us).
+  const bool both = chunks && (batch->n_seqs > 1 || max_rows <= attn::kChunkRows);
+  a.takes = both ? attn::kShort : attn::kEvery;
+  a.budget = budget;
   a.tickets = reinterpret_cast<uint32_t*>(wsb + wl.tickets);
   a.partial = reinterpret_cast<float*>(wsb + wl.partial);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // One sequence that may be a chunk: the chunk kernel takes it whatever its length turns out to be,
-  // and a prompt saves the other launch (about 5 us).
-  const bool both = max_rows > small && batch->n_seqs > 1;
-  if (both || max_rows <= small) {
+  if (both || !chunks) {
     const fl_status s = D == 64 ? (nt == 1 ? attn::launch<64, 1>(a, nsm, st) : attn::launch<64, 2>(a, nsm, st))
                                 : (nt == 1 ? attn::launch<128, 1>(a, nsm, st) : attn::launch<128, 2>(a, nsm, st));
     if (s || !both) return s;
   }
-  a.min_rows = both ? small + 1 : 1;
-  a.max_rows = 0x7fffffff;
+  a.takes = both ? attn::kChunk : attn::kEvery;
   a.tickets = reinterpret_cast<uint32_t*>(wsb + wl.tc_tickets);
   a.partial = reinterpret_cast<float*>(wsb + wl.tc_partial);
   return attn_tc::launch(a, D, nsm, st);

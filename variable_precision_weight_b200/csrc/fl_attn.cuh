@@ -17,10 +17,20 @@ struct Args {
   int64_t q_stride, out_stride;
   float scale_log2;  // scale * log2(e): the softmax runs on powers of two
   int window, sinks;
-  int min_rows, max_rows;  // the kernel takes sequences whose n * group is in [min_rows, max_rows]
+  int takes;          // which sequences this kernel takes (Takes)
+  long long budget;   // of chunk_takes
   uint32_t* tickets;  // [grid], zero between calls
   float* partial;     // two pieces per CTA
 };
+
+enum Takes : int { kEvery, kShort, kChunk };
+
+// Whether a sequence of `rows` query rows (new tokens times the group) per key/value head that see
+// np pages goes to the chunk kernel; the reasons stand at chunk_budget (fl_attn.cu).
+constexpr int kShortRows = 64, kChunkRows = 256, kFreeRows = 56;
+__host__ __device__ __forceinline__ bool chunk_takes(long long rows, long long np, long long budget) {
+  return rows > kShortRows && (rows > kChunkRows || (rows - kFreeRows) * np > budget);
+}
 
 // The pages that a sequence's new tokens see, as one list: pages [0, sink_pages) and
 // [win_page, blocks).
@@ -41,8 +51,8 @@ __device__ __forceinline__ Geo geo_of(const Args& a, int i, bool* bad) {
     g.sink_pages = min((min(a.sinks, g.s.len) + kv::kBlock - 1) / kv::kBlock, g.win_page);
   }
   g.np = blocks - g.win_page + g.sink_pages;
-  const long long rows = (long long)g.s.n * a.group;
-  if (rows < a.min_rows || rows > a.max_rows) g.s.n = 0;  // the other kernel's, or nothing to do
+  if (a.takes != kEvery && chunk_takes((long long)g.s.n * a.group, g.np, a.budget) != (a.takes == kChunk))
+    g.s.n = 0;  // the other kernel's
   if (g.s.n == 0) g.np = 0;
   return g;
 }
