@@ -6,6 +6,11 @@
 // so the keys are split freely. Codes enter the tensor-core products exactly (as bf16
 // values, fl_attn.cuh); the key's scale multiplies its score column, the value's its probability.
 //
+// Rounding: a probability times its value's scale enters the second product as bf16, the one type of
+// that product whose exponents hold every scale (fp16 would need the scales brought to one size for
+// each page). The error against 64 bits is 0.0022-0.0026 of the output's size, where rounding the
+// output alone gives 0.0017; rounding P alone gives 0.0016.
+//
 // Bound: HBM bytes of the visible records (512 + 128 D at D8, 512 + 64 D at D4 per page and head).
 // Measured: 8 streams of 45-49k tokens at D4, 112 us (63 us at the copy rate). The copies alone take
 // 88 us and the arithmetic alone 99: unpacking and the softmax, not the MMAs (16% of their pipe).
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const long long U = pre[n_seqs];
   // A CTA takes at least one unit per warp; where two per warp and item would do, one CTA per item,
   // so that items of equal lengths are not cut (a join through the workspace costs more than the
-  // second unit: one stream of 517 tokens took 14.0 us cut, 13.7 us so).
+  // second unit: one stream of 517 tokens took 13.2 us cut, 9.5 us so).
   const long long items = s_items;
   const int G = items <= gridDim.x && U <= 2 * kWarps * items ? (int)items
                                                               : (int)min((long long)gridDim.x, (U + kWarps - 1) / kWarps);

@@ -4,16 +4,20 @@
 // Mathematics: that of fl_attn.cu. Here the scores S = Q K^T and outputs O += P V are 128 x 128
 // tensor-core tiles. The codes enter both products exactly, as bf16 values c / f (f = 128 at D8,
 // 1024 at D4: fl_attn.cuh); f times the key's scale multiplies its score column, f times the
-// value's scale its probability, so nothing is rounded but P (to bf16) and the output.
+// value's scale its probability, so nothing is rounded but P (to bf16, as there and why) and the
+// output.
 // The running maximum is moved only when a row's grows by more than 8 (2^8 is no danger to fp32
 // sums), which leaves O in tensor memory untouched in nearly every step; l and o carry the same
 // power of two, so the result is the softmax all the same.
 //
 // Bound: per step of 128 keys and 256 query rows at D = 128 an SM needs 2048 cycles of MMA and
 // 2048 of the exponential unit. Measured: about 6.9 k cycles (2048 tokens over 32k, 16 heads of
-// 128: 766 us, 695 TFLOP/s). No unit is full: the exponentials, the unpacking and the products
+// 128: 770 us, 692 TFLOP/s). No unit is full: the exponentials, the unpacking and the products
 // each left out take 5% off, the softmax passes left out 20%; what bounds it is the latency of a
 // step's hand-offs (scores, softmax, products) with two tiles in flight, all tensor memory holds.
+// The 96 registers of the launch spill (264 bytes stored, 504 loaded a thread over the whole kernel).
+// A call of whole tiles takes 21.8 us and 3.60 a step (17.0 and 3.11 at D = 64); the join of a tile
+// of 256 rows cut into 3, 6, 12 parts 15, 22, 37 us (14, 19, 31), of 100 rows 3, 4, 8.
 //
 // How: one persistent CTA per SM, 20 warps. Unit = (sequence, key/value head, tile of 256 query
 // rows, step of 128 keys = two pages); rows are (token, head of the group) pairs. Each tile's
