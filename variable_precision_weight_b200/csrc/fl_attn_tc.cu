@@ -15,7 +15,7 @@
 // 128: 770 us, 692 TFLOP/s). No unit is full: the exponentials, the unpacking and the products
 // each left out take 5% off, the softmax passes left out 20%; what bounds it is the latency of a
 // step's hand-offs (scores, softmax, products) with two tiles in flight, all tensor memory holds.
-// The 96 registers of the launch spill (264 bytes stored, 504 loaded a thread over the whole kernel).
+// The 96 registers of the launch spill (256 bytes stored, 500 loaded a thread over the whole kernel).
 // A call of whole tiles takes 21.8 us and 3.60 a step (17.0 and 3.11 at D = 64); the join of a tile
 // of 256 rows cut into 3, 6, 12 parts 15, 22, 37 us (14, 19, 31), of 100 rows 3, 4, 8.
 //
@@ -854,7 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // then fall through on an older lap. The first step's scores mean that every unpacking warp
         // has passed its keys, so from there on the barriers are in the laps that are waited for; and
         // they stay: the keys kScaleRing steps on need an operand slot that frees after this half's P.
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)(cnt & 1)));
+        // The wait may span all the skipped steps, so its limit grows with them (20 us each, against 4).
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)(cnt & 1), kWaitLimitNs + 20000ull * (uint32_t)(step - cnt)));
         for (int j = 0; j < n && ok; ++j, ++cnt) {
           const int sr = (step + j) % kScaleRing, key0 = kStep * step_at(w.t, p0 + j);
           ok = __all_sync(0xffffffffu, mbar_wait(&sc_full[sr], (uint32_t)(((step + j) / kScaleRing) & 1)) &&
